@@ -43,6 +43,20 @@ SIGNATURES = {
                                     P, I32, P, U32, P]),
     "gdn_conv1d_fwd": (I32, [P, I32, P, P, I32, P, I32, I32, I64, I32, P, P, I32, P, P]),
     "gdn_conv1d_update": (I32, [P, I32, P, P, I32, P, P, I32, I32, I32, I32, P, P]),
+    "gdn_ssm_scan_workspace_size": (SZ, [I32, I64, I32, I32, I32, I32, I32]),
+    # x, xs, dt, dts, Bm, bs, Cm, cs, z, zs, dtype, A_log, dt_bias, D, h0, cu_seqlens,
+    # n_seq, B, T, H, G, P, N, y, hT, workspace, ws_bytes, stream
+    "gdn_ssm_scan": (I32, [P, I64, P, I64, P, I64, P, I64, P, I64, I32, P, P, P, P, P, I32, I32, I64,
+                           I32, I32, I32, I32, P, P, P, SZ, P]),
+    "gdn_ssm_decode_step_workspace_size": (SZ, [I32, I32, I32, I32, I32]),
+    # row, rs, dt, dts, z, zs, conv_w, conv_bias, W, conv_state, activation, A_log, dt_bias,
+    # D, n, H, G, P, N, state, state_idx, n_slots, y, workspace, ws_bytes, stream
+    "gdn_ssm_decode_step": (I32, [P, I64, P, I64, P, I64, P, P, I32, P, I32, P, P, P, I32, I32, I32,
+                                  I32, I32, P, P, I32, P, P, SZ, P]),
+    # x, xs, residual, rs, dtype, weight, eps, rows, D, q, scales, stream
+    "gdn_rmsnorm_fp8": (I32, [P, I64, P, I64, I32, P, F32, I64, I32, P, P, P]),
+    # a, as, a_scales, w, ws, w_scales, M, N, K, out, out_dtype, stream
+    "gdn_fp8_matmul": (I32, [P, I64, P, P, I64, P, I64, I32, I32, P, I32, P]),
     "gdn_device_status": (I32, [P]),
     "gdn_get_device_status": (I32, [P]),
     "gdn_selftest_wait_timeout": (I32, [U32, P]),

@@ -6,6 +6,7 @@ dtypes and devices, allocates outputs with torch, and forwards raw pointers.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Optional, Tuple
 
 import torch
@@ -418,3 +419,261 @@ def conv1d_update(x: torch.Tensor, w: torch.Tensor, conv_state: torch.Tensor,
               _ptr(conv_state), _ptr(state_idx), n, conv_state.shape[0], C,
               int(bool(activation)), _ptr(y), _stream(x))
     return y
+
+
+def _on(dev: torch.device):
+    """The operands' device made current for a launch, where it is not already."""
+    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _row_stride(t: torch.Tensor, name: str, inner: int) -> int:
+    """Element stride between the rows of t [B, T, ...] whose last `inner` dimensions
+    are one contiguous row.  Rows of all sequences must be evenly spaced."""
+    want = 1
+    for d in range(t.dim() - 1, t.dim() - 1 - inner, -1):
+        if t.shape[d] > 1 and t.stride(d) != want:
+            raise ValueError(f"{name}: each token's row must be contiguous")
+        want *= t.shape[d]
+    B, T = t.shape[0], t.shape[1]
+    if B * T <= 1:
+        return want
+    if T == 1:
+        st = t.stride(0)
+    else:
+        st = t.stride(1)
+        if B > 1 and t.stride(0) != T * st:
+            raise ValueError(f"{name}: the rows of consecutive sequences must be evenly spaced")
+    if st < want:
+        raise ValueError(f"{name}: rows overlap")
+    return st
+
+
+def ssm_scan_workspace_size(n_seq: int, T_total: int, H: int, G: int, P: int, N: int,
+                            dtype=torch.bfloat16) -> int:
+    return int(_lib.load().gdn_ssm_scan_workspace_size(n_seq, T_total, H, G, P, N, _DT[dtype]))
+
+
+def ssm_scan(x: torch.Tensor, dt: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor,
+             A_log: torch.Tensor, dt_bias: torch.Tensor, D: Optional[torch.Tensor] = None,
+             z: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+             cu_seqlens: Optional[torch.Tensor] = None, output_final_state: bool = True,
+             workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None
+             ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Selective state space scan over prompts:
+        dt <- softplus(dt + dt_bias);  h_t = exp(-exp(A_log) dt_t) h_{t-1} + dt_t B_t x_t^T;
+        y_t = (h_t^T C_t + D x_t) * silu(z_t).
+    x, z [B,T,H,P]; dt [B,T,H]; Bm, Cm [B,T,G,N] (head h reads group h / (H/G)), all of one
+    dtype (float32 or bfloat16) and each a slice of evenly spaced rows (the conv row's parts are
+    taken as they are); A_log, dt_bias, D [H] fp32; h0 [n_seq,H,N,P] fp32; cu_seqlens int32
+    [n_seq+1] (B == 1).  Returns (y [B,T,H,P] in x's dtype, hT [n_seq,H,N,P] fp32 or None)."""
+    _need(x, "x", contiguous=False)
+    dev = x.device
+    if x.dtype not in _DT:
+        raise TypeError("x must be float32 or bfloat16")
+    if x.dim() != 4 or Bm.dim() != 4:
+        raise ValueError("x must be [B, T, H, P] and Bm [B, T, G, N]")
+    B, T, H, P = x.shape
+    G, N = Bm.shape[2:]
+    for t, n, shape in ((dt, "dt", (B, T, H)), (Bm, "Bm", (B, T, G, N)), (Cm, "Cm", (B, T, G, N)),
+                        (z, "z", (B, T, H, P))):
+        if t is not None or n != "z":
+            _need(t, n, x.dtype, dev, contiguous=False)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{n} must be {list(shape)}")
+    for t, n in ((A_log, "A_log"), (dt_bias, "dt_bias"), (D, "D")):
+        if t is not None or n != "D":
+            _need(t, n, torch.float32, dev)
+            if tuple(t.shape) != (H,):
+                raise ValueError(f"{n} must be [H]")
+    n_seq = B
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        if B != 1:
+            raise ValueError("packed sequences need B == 1")
+        n_seq = cu_seqlens.numel() - 1
+    if h0 is not None:
+        _need(h0, "h0", torch.float32, dev)
+        if tuple(h0.shape) != (n_seq, H, N, P):
+            raise ValueError("h0 must be [n_seq, H, N, P]")
+    if out is None:
+        out = torch.empty((B, T, H, P), dtype=x.dtype, device=dev)
+    _need(out, "out", x.dtype, dev)
+    if tuple(out.shape) != (B, T, H, P):
+        raise ValueError("out must be [B, T, H, P]")
+    hT = torch.empty((n_seq, H, N, P), dtype=torch.float32, device=dev) if output_final_state else None
+    need = ssm_scan_workspace_size(n_seq, B * T, H, G, P, N, x.dtype)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _need(workspace, "workspace", None, dev)
+    with _on(dev):
+        _lib.call("gdn_ssm_scan", _ptr(x), _row_stride(x, "x", 2), _ptr(dt), _row_stride(dt, "dt", 1),
+                  _ptr(Bm), _row_stride(Bm, "Bm", 2), _ptr(Cm), _row_stride(Cm, "Cm", 2), _ptr(z),
+                  0 if z is None else _row_stride(z, "z", 2), _DT[x.dtype], _ptr(A_log),
+                  _ptr(dt_bias), _ptr(D), _ptr(h0), _ptr(cu_seqlens), n_seq, B, T, H, G, P, N,
+                  _ptr(out), _ptr(hT), _ptr(workspace),
+                  0 if workspace is None else workspace.numel() * workspace.element_size(),
+                  _stream(x))
+    return out, hT
+
+
+def ssm_decode_step_workspace_size(n: int, H: int, G: int, P: int, N: int) -> int:
+    return int(_lib.load().gdn_ssm_decode_step_workspace_size(n, H, G, P, N))
+
+
+def ssm_decode_step(row: torch.Tensor, dt: torch.Tensor, conv_w: torch.Tensor,
+                    conv_state: torch.Tensor, A_log: torch.Tensor, dt_bias: torch.Tensor,
+                    state: torch.Tensor, H: int, G: int, P: int, N: int,
+                    D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                    conv_bias: Optional[torch.Tensor] = None, activation: bool = True,
+                    state_indices: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                    ) -> torch.Tensor:
+    """One token of a state space layer: the short-convolution update of the projected rows
+    row [n, H*P + 2*G*N] bf16 ([x | B | C], before the convolution; conv_state [n_slots, C, W-1]
+    bf16 updated in place, conv_w [C, W] fp32), then one step of ssm_scan's recurrence on
+    state [n_slots,H,N,P] fp32, in place.  dt [n, H], z [n, H*P] bf16; rows may be slices of a
+    wider row.  state_indices int32 [n] names each request's slot (-1: padding, y = 0);
+    without it request r owns slot r.  Returns y [n,H,P] bf16."""
+    _need(row, "row", torch.bfloat16, contiguous=False)
+    dev = row.device
+    C = H * P + 2 * G * N
+    if row.dim() != 2 or row.shape[1] != C:
+        raise ValueError("row must be [n, H*P + 2*G*N]")
+    n = row.shape[0]
+    strides = []
+    for t, nm, width in ((row, "row", C), (dt, "dt", H), (z, "z", H * P)):
+        if t is None and nm == "z":
+            strides.append(0)
+            continue
+        _need(t, nm, torch.bfloat16, dev, contiguous=False)
+        if tuple(t.shape) != (n, width):
+            raise ValueError(f"{nm} must be [n, {width}]")
+        if width > 1 and t.stride(1) != 1:
+            raise ValueError(f"{nm} needs a contiguous last dimension")
+        strides.append(t.stride(0) if n > 1 else max(width, t.stride(0)))
+    _need(conv_w, "conv_w", torch.float32, dev)
+    if conv_w.dim() != 2 or conv_w.shape[0] != C:
+        raise ValueError("conv_w must be [C, W] with C = H*P + 2*G*N")
+    W = conv_w.shape[1]
+    _need(conv_state, "conv_state", torch.bfloat16, dev)
+    _need(state, "state", torch.float32, dev)
+    if state.dim() != 4 or tuple(state.shape[1:]) != (H, N, P):
+        raise ValueError("state must be [n_slots, H, N, P]")
+    n_slots = state.shape[0]
+    if conv_state.dim() != 3 or tuple(conv_state.shape) != (n_slots, C, W - 1):
+        raise ValueError("conv_state must be [n_slots, C, W-1]")
+    for t, nm, size in ((A_log, "A_log", H), (dt_bias, "dt_bias", H), (D, "D", H),
+                        (conv_bias, "conv_bias", C)):
+        if t is None and nm in ("D", "conv_bias"):
+            continue
+        _need(t, nm, torch.float32, dev)
+        if tuple(t.shape) != (size,):
+            raise ValueError(f"{nm} must be [{size}]")
+    if state_indices is None:
+        if n_slots < n:
+            raise ValueError("without state_indices, state must have at least n slots")
+    else:
+        _need(state_indices, "state_indices", torch.int32, dev)
+        if tuple(state_indices.shape) != (n,):
+            raise ValueError("state_indices must be int32 [n]")
+    if out is None:
+        out = torch.empty((n, H, P), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, dev)
+    if tuple(out.shape) != (n, H, P):
+        raise ValueError("out must be [n, H, P]")
+    if workspace is None:
+        workspace = torch.empty(max(ssm_decode_step_workspace_size(n, H, G, P, N), 1),
+                                dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", None, dev)
+    with _on(dev):
+        _lib.call("gdn_ssm_decode_step", _ptr(row), strides[0], _ptr(dt), strides[1], _ptr(z),
+                  strides[2], _ptr(conv_w), _ptr(conv_bias), W, _ptr(conv_state),
+                  int(bool(activation)), _ptr(A_log), _ptr(dt_bias), _ptr(D), n, H, G, P, N,
+                  _ptr(state), _ptr(state_indices), n_slots, _ptr(out), _ptr(workspace),
+                  workspace.numel() * workspace.element_size(), _stream(row))
+    return out
+
+
+def rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                eps: float = 1e-6, out: Optional[torch.Tensor] = None,
+                scales: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Root-mean-square norm with the residual's addition and an 8-bit output:
+    s = x + residual (residual <- s, in place), y = s / sqrt(mean(s^2) + eps) * weight, and per
+    block of 128 elements of a row scale = max|y| / 448 (1 for a block of zeros), q = e4m3(y / scale).
+    x, residual [..., D] float32 or bfloat16 (2-D operands may have a row stride); weight [D] fp32.
+    Returns (q [..., D] float8_e4m3fn, scales [..., ceil(D/128)] fp32), fp8_matmul's first operand."""
+    _need(x, "x", contiguous=False)
+    dev = x.device
+    if x.dtype not in _DT:
+        raise TypeError("x must be float32 or bfloat16")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., D]")
+    D = x.shape[-1]
+    rows = x.numel() // D
+    _need(weight, "weight", torch.float32, dev)
+    if tuple(weight.shape) != (D,):
+        raise ValueError("weight must be [D]")
+    strides = []
+    for t, n in ((x, "x"), (residual, "residual")):
+        if t is None:
+            strides.append(0)
+            continue
+        _need(t, n, x.dtype, dev, contiguous=t.dim() != 2)
+        if t.shape != x.shape:
+            raise ValueError("residual must have x's shape")
+        if t.dim() == 2 and ((D > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < D)):
+            raise ValueError(f"{n} rows must be contiguous and must not overlap")
+        strides.append(t.stride(0) if t.dim() == 2 and rows > 1 else D)
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+    if scales is None:
+        scales = torch.empty((*x.shape[:-1], -(-D // 128)), dtype=torch.float32, device=dev)
+    _need(out, "out", torch.float8_e4m3fn, dev)
+    _need(scales, "scales", torch.float32, dev)
+    if out.shape != x.shape or tuple(scales.shape) != (*x.shape[:-1], -(-D // 128)):
+        raise ValueError("out must have x's shape and scales [..., ceil(D/128)]")
+    with _on(dev):
+        _lib.call("gdn_rmsnorm_fp8", _ptr(x), strides[0], _ptr(residual), strides[1], _DT[x.dtype],
+                  _ptr(weight), float(eps), rows, D, _ptr(out), _ptr(scales), _stream(x))
+    return out, scales
+
+
+def fp8_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+               out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None
+               ) -> torch.Tensor:
+    """out = (a * a_scales) @ (w * w_scales)^T on e4m3 operands, fp32 accumulation.
+    a [..., K] float8_e4m3fn with a_scales [..., ceil(K/128)] fp32 (one per row and block of 128,
+    as rmsnorm_fp8 gives them); w [N, K] float8_e4m3fn with w_scales [ceil(N/128), ceil(K/128)]
+    fp32 (one per 128 x 128 block).  2-D a and w may have a row stride.  Returns [..., N] in
+    out_dtype (float32 or bfloat16)."""
+    _need(a, "a", torch.float8_e4m3fn, contiguous=a.dim() != 2)
+    dev = a.device
+    _need(w, "w", torch.float8_e4m3fn, dev, contiguous=False)
+    if out_dtype not in _DT:
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    if a.dim() < 1 or w.dim() != 2 or a.shape[-1] != w.shape[1] or 0 in w.shape:
+        raise ValueError("a must be [..., K] and w [N, K]")
+    N, K = w.shape
+    M = a.numel() // K
+    kb = -(-K // 128)
+    _need(a_scales, "a_scales", torch.float32, dev)
+    _need(w_scales, "w_scales", torch.float32, dev)
+    if tuple(a_scales.shape) != (*a.shape[:-1], kb):
+        raise ValueError("a_scales must be [..., ceil(K/128)]")
+    if tuple(w_scales.shape) != (-(-N // 128), kb):
+        raise ValueError("w_scales must be [ceil(N/128), ceil(K/128)]")
+    strides = []
+    for t, n, rows in ((a, "a", M), (w, "w", N)):
+        if t.dim() == 2 and ((K > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < K)):
+            raise ValueError(f"{n} rows must be contiguous and must not overlap")
+        strides.append(t.stride(0) if t.dim() == 2 and rows > 1 else K)
+    if out is None:
+        out = torch.empty((*a.shape[:-1], N), dtype=out_dtype, device=dev)
+    _need(out, "out", out_dtype, dev)
+    if tuple(out.shape) != (*a.shape[:-1], N):
+        raise ValueError("out must be [..., N]")
+    with _on(dev):
+        _lib.call("gdn_fp8_matmul", _ptr(a), strides[0], _ptr(a_scales), _ptr(w), strides[1],
+                  _ptr(w_scales), M, N, K, _ptr(out), _DT[out_dtype], _stream(a))
+    return out

@@ -16,6 +16,10 @@
 #include "chunk_tc.cuh"
 #include "conv1d.cuh"
 #include "decode_step.cuh"
+#include "ssm_scan.cuh"
+#include "ssm_decode.cuh"
+#include "rmsnorm_fp8.cuh"
+#include "fp8_matmul.cuh"
 
 namespace {
 
@@ -610,6 +614,203 @@ gdn_status gdn_device_status(void* stream) {
 }
 
 gdn_status gdn_get_device_status(void* stream) { return gdn_device_status(stream); }
+
+}  // extern "C"
+
+// ---------------------------------------------- state space layer operators
+
+namespace {
+
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+template <typename T>
+gdn_status launch_scan_simt(const gdn::ssm::ScanArgs& a, cudaStream_t st) {
+    const int64_t nb = (int64_t)a.n_seq * a.H * (a.P / 32);
+    if (nb > 0x7fffffff) return GDN_ERR_UNSUPPORTED;
+    if (a.N == 128) gdn::ssm::scan_kernel<128, T><<<(unsigned)nb, 128, 0, st>>>(a);
+    else if (a.N == 64) gdn::ssm::scan_kernel<64, T><<<(unsigned)nb, 128, 0, st>>>(a);
+    else gdn::ssm::scan_kernel<32, T><<<(unsigned)nb, 128, 0, st>>>(a);
+    return launch_check();
+}
+
+template <int N, int P>
+gdn_status launch_ssm_state(const gdn::ssm::DecodeArgs& a, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.n * a.H * (P == 128 ? 2 : 1)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cuda_check(cudaLaunchKernelEx(&cfg, gdn::ssm::decode_state_kernel<N, P>, a));
+}
+
+template <typename T, int U, bool VEC>
+gdn_status launch_rmsnorm(const gdn::nrm::Args& a, int nt, cudaStream_t st) {
+    const int64_t most = (int64_t)num_sms() * 32;
+    gdn::nrm::rmsnorm_kernel<T, U, VEC><<<(unsigned)(a.rows < most ? a.rows : most), nt, 0, st>>>(a);
+    return launch_check();
+}
+
+template <typename T, bool VEC>
+gdn_status rmsnorm_sized(const gdn::nrm::Args& a, cudaStream_t st) {
+    const int units = (a.D + 7) / 8;
+    const int u = units <= 256 ? 1 : (units <= 512 ? 2 : (units <= 4096 ? 4 : 8));
+    const int nt = ((units + u - 1) / u + 31) / 32 * 32;
+    if (u == 1) return launch_rmsnorm<T, 1, VEC>(a, nt, st);
+    if (u == 2) return launch_rmsnorm<T, 2, VEC>(a, nt, st);
+    if (u == 4) return launch_rmsnorm<T, 4, VEC>(a, nt, st);
+    return launch_rmsnorm<T, 8, VEC>(a, nt, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_ssm_scan_workspace_size(int n_seq, int64_t T_total, int H, int G, int P, int N,
+                                   gdn_dtype dtype) {
+    (void)n_seq; (void)T_total; (void)H; (void)G; (void)P; (void)N; (void)dtype;
+    return 0;
+}
+
+gdn_status gdn_ssm_scan(const void* x, int64_t x_stride, const void* dt, int64_t dt_stride,
+                        const void* Bm, int64_t b_stride, const void* Cm, int64_t c_stride,
+                        const void* z, int64_t z_stride, gdn_dtype dtype, const float* A_log,
+                        const float* dt_bias, const float* D, const float* h0,
+                        const int32_t* cu_seqlens, int n_seq, int B, int64_t T, int H, int G,
+                        int P, int N, void* y, float* hT, void* workspace, size_t ws_bytes,
+                        void* stream) {
+    if (B < 0 || T < 0 || n_seq < 0 || H < 1 || G < 1 || H % G) return GDN_ERR_INVALID_ARG;
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (!head_dim_ok(P) || !head_dim_ok(N)) return GDN_ERR_UNSUPPORTED;
+    if (cu_seqlens) {
+        if (B != 1) return GDN_ERR_INVALID_ARG;
+    } else {
+        n_seq = B;
+    }
+    if (n_seq == 0) return GDN_OK;
+    const int64_t hp = (int64_t)H * P, gn = (int64_t)G * N;
+    if (x_stride < hp || dt_stride < H || b_stride < gn || c_stride < gn || (z && z_stride < hp))
+        return GDN_ERR_INVALID_ARG;
+    if (T > ((int64_t)1 << 40) / B) return GDN_ERR_UNSUPPORTED;
+    const int64_t rows = (int64_t)B * T;
+    if (!A_log || !dt_bias) return GDN_ERR_INVALID_ARG;
+    if (rows > 0 && (!x || !dt || !Bm || !Cm || !y || y == x || y == z || y == Bm || y == Cm))
+        return GDN_ERR_INVALID_ARG;
+    const size_t es = dtype == GDN_BF16 ? 2 : 4;
+    for (const void* p : {x, dt, Bm, Cm, z, (const void*)y})
+        if (p && !aligned_to(p, es)) return GDN_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)A_log, (const void*)dt_bias, (const void*)D,
+                          (const void*)h0, (const void*)cu_seqlens, (const void*)hT})
+        if (p && !aligned_to(p, 4)) return GDN_ERR_INVALID_ARG;
+    if (hT && hT == h0) return GDN_ERR_INVALID_ARG;
+    const size_t need = gdn_ssm_scan_workspace_size(n_seq, rows, H, G, P, N, dtype);
+    if (need && (!workspace || ws_bytes < need || !aligned16(workspace))) return GDN_ERR_INVALID_ARG;
+    gdn::ssm::ScanArgs a{x,    Bm,      Cm, dt, z,  x_stride,   b_stride, c_stride, dt_stride,
+                         z_stride, A_log, dt_bias, D, h0, cu_seqlens, n_seq, T, H, G, P, N, y, hT};
+    cudaStream_t st = as_stream(stream);
+    return dtype == GDN_BF16 ? launch_scan_simt<__nv_bfloat16>(a, st) : launch_scan_simt<float>(a, st);
+}
+
+size_t gdn_ssm_decode_step_workspace_size(int n, int H, int G, int P, int N) {
+    if (n <= 0 || H < 1 || G < 1 || P < 1 || N < 1) return 0;
+    return align256((size_t)n * ((size_t)H * P + 2 * (size_t)G * N) * 4);
+}
+
+gdn_status gdn_ssm_decode_step(const void* row, int64_t row_stride, const void* dt,
+                               int64_t dt_stride, const void* z, int64_t z_stride,
+                               const float* conv_w, const float* conv_bias, int W,
+                               void* conv_state, int activation, const float* A_log,
+                               const float* dt_bias, const float* D, int n, int H, int G, int P,
+                               int N, float* state, const int32_t* state_idx, int n_slots, void* y,
+                               void* workspace, size_t ws_bytes, void* stream) {
+    if (n < 0 || H < 1 || G < 1 || H % G) return GDN_ERR_INVALID_ARG;
+    if (!head_dim_ok(P) || !head_dim_ok(N)) return GDN_ERR_UNSUPPORTED;
+    if (W < 1 || W > 4 || (activation != 0 && activation != 1)) return GDN_ERR_INVALID_ARG;
+    const int64_t hp = (int64_t)H * P, C = hp + 2 * (int64_t)G * N;
+    if (row_stride < C || dt_stride < H || (z && z_stride < hp)) return GDN_ERR_INVALID_ARG;
+    if (n == 0) return GDN_OK;
+    if (!row || !dt || !conv_w || !A_log || !dt_bias || !y || n_slots < 0 || (!state_idx && n_slots < n))
+        return GDN_ERR_INVALID_ARG;
+    if (n_slots > 0 && (!state || !aligned16(state) || (W > 1 && !conv_state))) return GDN_ERR_INVALID_ARG;
+    for (const void* p : {row, dt, z, (const void*)conv_state, (const void*)y})
+        if (p && !aligned_to(p, 2)) return GDN_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)conv_w, (const void*)conv_bias, (const void*)A_log,
+                          (const void*)dt_bias, (const void*)D, (const void*)state_idx})
+        if (p && !aligned_to(p, 4)) return GDN_ERR_INVALID_ARG;
+    if (y == row || y == z) return GDN_ERR_INVALID_ARG;
+    if (!workspace || ws_bytes < gdn_ssm_decode_step_workspace_size(n, H, G, P, N) || !aligned16(workspace))
+        return GDN_ERR_INVALID_ARG;
+    if ((int64_t)n * H * 2 > 0x7fffffff || C > 0x7fffffff / 4 ||
+        n > 65535 * gdn::ssm::kDecReqs)
+        return GDN_ERR_UNSUPPORTED;
+    using bf = __nv_bfloat16;
+    const gdn::ssm::DecodeArgs a{(const bf*)row, (const bf*)dt, (const bf*)z, row_stride, dt_stride,
+                                 z_stride, conv_w, conv_bias, (bf*)conv_state, state_idx, W,
+                                 activation, n, n_slots, (int)C, A_log, dt_bias, D, H, G, state,
+                                 static_cast<float*>(workspace), (bf*)y};
+    cudaStream_t st = as_stream(stream);
+    const dim3 grid((unsigned)((C + 127) / 128), (unsigned)((n + gdn::ssm::kDecReqs - 1) / gdn::ssm::kDecReqs));
+    switch (W) {
+        case 1: gdn::ssm::decode_conv_kernel<1><<<grid, 128, 0, st>>>(a); break;
+        case 2: gdn::ssm::decode_conv_kernel<2><<<grid, 128, 0, st>>>(a); break;
+        case 3: gdn::ssm::decode_conv_kernel<3><<<grid, 128, 0, st>>>(a); break;
+        default: gdn::ssm::decode_conv_kernel<4><<<grid, 128, 0, st>>>(a); break;
+    }
+    gdn_status s = launch_check();
+    if (s != GDN_OK) return s;
+#define GDN_SSM(NN, PP) \
+    if (N == NN && P == PP) return launch_ssm_state<NN, PP>(a, st);
+    GDN_SSM(128, 128) GDN_SSM(128, 64) GDN_SSM(128, 32)
+    GDN_SSM(64, 128) GDN_SSM(64, 64) GDN_SSM(64, 32)
+    GDN_SSM(32, 128) GDN_SSM(32, 64) GDN_SSM(32, 32)
+#undef GDN_SSM
+    return GDN_ERR_UNSUPPORTED;
+}
+
+gdn_status gdn_rmsnorm_fp8(const void* x, int64_t x_stride, void* residual, int64_t r_stride,
+                           gdn_dtype dtype, const float* weight, float eps, int64_t rows, int D,
+                           void* q, float* scales, void* stream) {
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (rows < 0 || D < 1 || x_stride < D || (residual && r_stride < D) || !(eps >= 0.f))
+        return GDN_ERR_INVALID_ARG;
+    if (rows == 0) return GDN_OK;
+    if (!x || !weight || !q || !scales || residual == x) return GDN_ERR_INVALID_ARG;
+    const size_t es = dtype == GDN_BF16 ? 2 : 4;
+    if (!aligned_to(x, es) || !aligned_to(residual, es) || !aligned_to(weight, 4) || !aligned_to(scales, 4))
+        return GDN_ERR_INVALID_ARG;
+    if (D > 65536) return GDN_ERR_UNSUPPORTED;  // the row is held in one block's registers
+    const gdn::nrm::Args a{x, residual, weight, rows, D, x_stride, r_stride, eps,
+                           static_cast<uint8_t*>(q), scales};
+    // 16-byte accesses where every row starts on 16 bytes (8 for the 8-bit rows)
+    const bool vec = D % 8 == 0 && aligned16(x) && x_stride * es % 16 == 0 && aligned16(weight) &&
+                     aligned_to(q, 8) && (!residual || (aligned16(residual) && r_stride * es % 16 == 0));
+    cudaStream_t st = as_stream(stream);
+    if (dtype == GDN_BF16)
+        return vec ? rmsnorm_sized<__nv_bfloat16, true>(a, st) : rmsnorm_sized<__nv_bfloat16, false>(a, st);
+    return vec ? rmsnorm_sized<float, true>(a, st) : rmsnorm_sized<float, false>(a, st);
+}
+
+gdn_status gdn_fp8_matmul(const void* a, int64_t a_stride, const float* a_scales, const void* w,
+                          int64_t w_stride, const float* w_scales, int64_t M, int N, int K,
+                          void* out, gdn_dtype out_dtype, void* stream) {
+    if (out_dtype != GDN_F32 && out_dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (M < 0 || N < 1 || K < 1 || a_stride < K || w_stride < K) return GDN_ERR_INVALID_ARG;
+    if (M == 0) return GDN_OK;
+    if (!a || !a_scales || !w || !w_scales || !out) return GDN_ERR_INVALID_ARG;
+    if (!aligned_to(a_scales, 4) || !aligned_to(w_scales, 4) || !aligned_to(out, out_dtype == GDN_BF16 ? 2 : 4))
+        return GDN_ERR_INVALID_ARG;
+    if (M > 65535 * 64) return GDN_ERR_UNSUPPORTED;
+    const gdn::mm8::Args g{static_cast<const uint8_t*>(a), a_scales, static_cast<const uint8_t*>(w),
+                           w_scales, a_stride, w_stride, (int)M, N, K, out};
+    cudaStream_t st = as_stream(stream);
+    const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 63) / 64));
+    if (out_dtype == GDN_BF16) gdn::mm8::fp8_matmul_simt_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(g);
+    else gdn::mm8::fp8_matmul_simt_kernel<float><<<grid, 256, 0, st>>>(g);
+    return launch_check();
+}
 
 }  // extern "C"
 

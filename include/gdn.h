@@ -379,6 +379,117 @@ gdn_status gdn_state_combine(const float* A, const float* X, const float* C, flo
 gdn_status gdn_accumulate_f32(float* y, const float* x, int64_t n, void* stream);
 
 /*
+ * gdn_ssm_scan -- the selective state space scan over prompts: a scalar decay
+ * per head and token, and no delta term.  Per sequence and head (h = S^T,
+ * [N, P], key-major, as the states above; head h reads group h / (H/G) of Bm
+ * and Cm):
+ *     dt_t = softplus(dt_raw_t + dt_bias)     (softplus as in gdn_gate_prep)
+ *     h_t  = exp(-exp(A_log) dt_t) h_{t-1} + dt_t Bm_t x_t^T
+ *     y_t  = (h_t^T Cm_t + D x_t) * silu(z_t)
+ * x, Bm and Cm are the row that gdn_conv1d_fwd leaves; every operand has its own
+ * token stride, so slices of one projected row are taken as they are.
+ *   x, z      : `dtype` (GDN_F32 or GDN_BF16), element (t, h, p) at
+ *               t * stride + h * P + p; z NULL for no gate.
+ *   Bm, Cm    : `dtype`, element (t, g, n) at t * stride + g * N + n.
+ *   dt        : `dtype`, element (t, h) at t * stride + h, before the bias.
+ *               Strides in elements, at least one row.  t runs over the B*T
+ *               rows of a dense batch, or the T rows of a packed one.
+ *   A_log, dt_bias : fp32 [H].   D : fp32 [H], NULL for no skip.
+ *   h0        : fp32 [n_seq, H, N, P] or NULL for zeros.
+ *   cu_seqlens: as gdn_chunk_fwd (NULL: n_seq = B sequences of T rows).
+ *   y         : `dtype` [rows, H, P] contiguous, written; not x, z, Bm or Cm.
+ *   hT        : fp32 [n_seq, H, N, P], written; NULL to skip; not h0.
+ *   workspace : >= gdn_ssm_scan_workspace_size(...) bytes, 16-byte aligned (NULL
+ *               where that is 0); its contents on entry do not matter.  Calls
+ *               that may run at the same time need one each.
+ * P, N in {32, 64, 128}.  Sums, decays and states are fp32 in every kernel.
+ * Sequences are independent: what one holds, a NaN included, reaches no other.
+ * Errors: INVALID_ARG (NULL or misaligned pointers, sizes < 0, H % G != 0, a
+ * stride shorter than a row, B != 1 with cu_seqlens, a short workspace),
+ * UNSUPPORTED (other P or N).  As in gdn_chunk_fwd, offsets outside [0, T] are
+ * undefined behaviour.
+ */
+size_t gdn_ssm_scan_workspace_size(int n_seq, int64_t T_total, int H, int G, int P, int N,
+                                   gdn_dtype dtype);
+gdn_status gdn_ssm_scan(const void* x, int64_t x_stride, const void* dt, int64_t dt_stride,
+                        const void* Bm, int64_t b_stride, const void* Cm, int64_t c_stride,
+                        const void* z, int64_t z_stride, gdn_dtype dtype, const float* A_log,
+                        const float* dt_bias, const float* D, const float* h0,
+                        const int32_t* cu_seqlens, int n_seq, int B, int64_t T, int H, int G,
+                        int P, int N, void* y, float* hT, void* workspace, size_t ws_bytes,
+                        void* stream);
+
+/*
+ * gdn_ssm_decode_step -- one token of a state space layer: the short-convolution
+ * update of the projected row, then one step of gdn_ssm_scan's recurrence on the
+ * request's state.  The convolved row stays in fp32 (it is not rounded between
+ * the two), so a step after gdn_conv1d_fwd + gdn_ssm_scan differs from one more
+ * scanned token by that rounding only.
+ *   row        : bf16 [n, *] before the convolution, row stride row_stride
+ *                elements, each [x: H*P | B: G*N | C: G*N], C_all channels in all.
+ *   dt         : bf16 [n, *], H values a row.   z : bf16 [n, *], H*P values a row,
+ *                or NULL.
+ *   conv_w     : fp32 [C_all, W], W in 1..4;  conv_bias fp32 [C_all] or NULL;
+ *                activation 1 = SiLU, 0 = none.
+ *   conv_state : bf16 [n_slots, C_all, W-1], in place (NULL allowed when W == 1).
+ *   state, state_idx, n_slots : fp32 [n_slots, H, N, P] in place, as
+ *                gdp_decode_step_indexed: a negative slot is padding (y = 0,
+ *                nothing touched); a slot >= n_slots is treated the same and
+ *                recorded in the device status word; slots must be distinct.
+ *   y          : bf16 [n, H, P], written; not row or z.
+ *   workspace  : >= gdn_ssm_decode_step_workspace_size(...) bytes, 16-byte
+ *                aligned (the convolved rows); its contents on entry do not
+ *                matter.  Calls that may run at the same time need one each.
+ * Errors: as gdn_ssm_scan and gdp_decode_layer_step.
+ */
+size_t gdn_ssm_decode_step_workspace_size(int n, int H, int G, int P, int N);
+gdn_status gdn_ssm_decode_step(const void* row, int64_t row_stride, const void* dt,
+                               int64_t dt_stride, const void* z, int64_t z_stride,
+                               const float* conv_w, const float* conv_bias, int W,
+                               void* conv_state, int activation, const float* A_log,
+                               const float* dt_bias, const float* D, int n, int H, int G, int P,
+                               int N, float* state, const int32_t* state_idx, int n_slots, void* y,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * gdn_rmsnorm_fp8 -- the norm ahead of a layer's projection: the residual's
+ * addition, a root-mean-square norm, and an output in e4m3 with one fp32 scale
+ * per row and block of 128 elements (the operand of gdn_fp8_matmul).
+ *     s = x + residual, residual <- s (rounded to dtype);  y = s rsqrt(mean s^2 + eps) w
+ *     scale = max|y| / 448 over the block (1 for a block of zeros);  q = e4m3(y / scale)
+ * s and y are fp32; the norm is of the unrounded sum.  The last block of a row
+ * may be shorter.  A NaN or infinity in a row makes that row's scales and values
+ * NaN where it reaches them, and no other row's.
+ *   x        : `dtype` [rows, D], row stride x_stride >= D elements.
+ *   residual : `dtype` [rows, D], row stride r_stride, in place; NULL for none;
+ *              not x.
+ *   weight   : fp32 [D].   q : e4m3 bytes [rows, D].
+ *   scales   : fp32 [rows, ceil(D / 128)].
+ * Errors: INVALID_ARG (NULL or misaligned pointers, sizes, strides, eps < 0),
+ * UNSUPPORTED (D > 65536).
+ */
+gdn_status gdn_rmsnorm_fp8(const void* x, int64_t x_stride, void* residual, int64_t r_stride,
+                           gdn_dtype dtype, const float* weight, float eps, int64_t rows, int D,
+                           void* q, float* scales, void* stream);
+
+/*
+ * gdn_fp8_matmul -- a layer's projection on 8-bit operands:
+ *     out[m, n] = sum_b a_scales[m, b] w_scales[n / 128, b] sum_{k in block b} a[m, k] w[n, k]
+ * over the ceil(K / 128) blocks of 128 of K; products and sums in fp32, one
+ * rounding to out_dtype.
+ *   a : e4m3 bytes [M, K], row stride a_stride >= K;   a_scales fp32 [M, ceil(K/128)].
+ *   w : e4m3 bytes [N, K], row stride w_stride >= K;
+ *       w_scales fp32 [ceil(N/128), ceil(K/128)].
+ *   out : [M, N] of out_dtype (GDN_F32 or GDN_BF16), contiguous.
+ * M == 0 is a no-op.  Operands whose rows start on 16 bytes run on the tensor
+ * cores; others on a plain fp32 kernel, much slower.
+ * Errors: INVALID_ARG (NULL or misaligned pointers, sizes, strides).
+ */
+gdn_status gdn_fp8_matmul(const void* a, int64_t a_stride, const float* a_scales, const void* w,
+                          int64_t w_stride, const float* w_scales, int64_t M, int N, int K,
+                          void* out, gdn_dtype out_dtype, void* stream);
+
+/*
  * gdn_device_status -- reads and clears the device status word on the current
  * device.  Kernels that wait on the device (mbarrier waits in the tensor-core
  * kernel) give up after a bounded number of polls, record GDN_ERR_TIMEOUT
