@@ -1,0 +1,349 @@
+// fp8_matmul_tc.cuh -- the block-scaled 8-bit product on the tensor cores.
+//
+//     out[m, n] = sum_b as[m, b] ws[n / 128, b] (sum_{k in block b} a[m, k] w[n, k])
+//
+// The scales change every 128 of K, so the tensor core accumulates one block of
+// K at a time into tensor memory (four K = 32 products, kind::f8f6f4) and the
+// promotion warps add it, scaled, to fp32 sums in registers.  Two accumulators
+// alternate, so the products of block b + 1 run while block b is promoted.
+//
+// One operand's rows are the 128 tensor-memory lanes, the other's the TN columns:
+//  * TOKENS = true, TN = 256: lanes are tokens.  A thread's scale is one number a
+//    block (its columns lie in one 128-block of n).  The form of prompts.
+//  * TOKENS = false, TN = 16..128: lanes are rows of w, columns are tokens, so a
+//    few tokens fill whole tiles and w streams through once.  The K range may be
+//    split over a cluster of up to 8 CTAs; each leaves its partial sums in
+//    shared memory and the cluster adds them in rank order (no atomics).
+// Warps: promotion (4 or 8), then a TMA warp and an MMA warp.  A CTA walks its
+// tiles (blockIdx.x, + gridDim.x, ...): loads and products of the next tile run
+// while the last one is written out.
+#pragma once
+
+#include "chunk_tc.cuh"
+#include "fp8_matmul.cuh"
+
+namespace gdn {
+namespace mm8 {
+
+constexpr uint32_t kLaneTile = 128 * 128;  // bytes of one 128-row tile of a K block
+
+template <bool TOKENS, int TN>
+struct Cfg {
+    static constexpr int NPW = TN >= 128 ? 8 : 4;         // promotion warps
+    static constexpr int CPT = TN / (NPW / 4);            // columns of one promotion thread
+    static constexpr int THREADS = 32 * (NPW + 2);
+    static constexpr uint32_t STAGE = kLaneTile + TN * 128;
+    static constexpr int NS = TN == 256 ? 4 : 6;          // ring stages
+    static constexpr uint32_t OFF_SC = NS * STAGE;        // per-warp column scales (columns = tokens)
+    static constexpr uint32_t OFF_BAR = OFF_SC + (TOKENS ? 0 : NPW * 2 * CPT * 4);
+    static constexpr uint32_t SMEM = OFF_BAR + (2 * NS + 5) * 8 + 16 + 1024;
+    static constexpr uint32_t COLS = 2 * TN < 32 ? 32 : 2 * TN;
+    static_assert(TOKENS || TN * 512 <= NS * STAGE, "partial sums fit in the ring");
+    static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+struct TcArgs {
+    CUtensorMap lanes, cols;  // [rows, K] e4m3, boxes of 128 bytes x 128 (TN) rows, 128-byte swizzle
+    Args g;
+    int tiles_l, tiles;       // tiles along the lane operand, tiles in all
+    int split;                // CTAs of a cluster, each with its part of K
+};
+
+// kind::f8f6f4: e4m3 x e4m3 -> fp32, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+template <int ACC>
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "n"(ACC)
+        : "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t caddr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(caddr) : "memory");
+    return v;
+}
+
+template <bool TOKENS, int TN, typename TOut>
+__global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), 1) fp8_matmul_tc_kernel(
+    const __grid_constant__ TcArgs p) {
+    using C = Cfg<TOKENS, TN>;
+    constexpr int NS = C::NS, NPW = C::NPW, CPT = C::CPT;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_u32 = smem_u32(smem_raw);
+    const uint32_t sbase = (raw_u32 + 1023u) & ~1023u;
+    uint8_t* base = smem_raw + (sbase - raw_u32);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::OFF_BAR);
+    uint64_t *full = bars, *empty = bars + NS, *acc_full = bars + 2 * NS, *acc_free = acc_full + 2,
+             *drain = acc_full + 4;
+    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * NS + 5);
+    volatile uint32_t* abort_flag = misc + 1;
+    const Args& g = p.g;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kb_all = (g.K + 127) / 128;
+    const int split = p.split;
+    const int rank = split > 1 ? (int)tc::cluster_ctarank() : 0;
+    const int kb0 = (int)((int64_t)kb_all * rank / split);
+    const int kb1 = (int)((int64_t)kb_all * (rank + 1) / split);
+    const int tile0 = blockIdx.x / split, tile_step = gridDim.x / split;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_free[i], NPW);
+        }
+        mbar_init(drain, 1);
+        misc[1] = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) tc::tmem_alloc(&misc[0], C::COLS);
+    tc::tc_before_sync();
+    __syncthreads();
+    tc::tc_after_sync();
+    const uint32_t tmem = __reduce_max_sync(0xffffffffu, misc[0]);
+
+    if (warp == NPW) {
+        // ---------------------------------------------------------- TMA warp
+        if (lane == 0) {
+            tc::prefetch_tmap(&p.lanes);
+            tc::prefetch_tmap(&p.cols);
+            int it = 0;
+            for (int t = tile0; t < p.tiles && !*abort_flag; t += tile_step) {
+                const int lrow = 128 * (t % p.tiles_l), crow = TN * (t / p.tiles_l);
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int s = it % NS;
+                    if (it >= NS && !tcf::wait(&empty[s], ((it / NS) - 1) & 1, abort_flag)) break;
+                    uint8_t* st = base + s * C::STAGE;
+                    tc::mbar_arrive_expect_tx(&full[s], C::STAGE);
+                    tc::tma_load_2d(st, &p.lanes, 128 * kb, lrow, &full[s]);
+                    tc::tma_load_2d(st + kLaneTile, &p.cols, 128 * kb, crow, &full[s]);
+                }
+            }
+            // never leave with a copy in flight
+            for (int i = it > NS ? it - NS : 0; i < it; ++i) tcf::drain_wait(&full[i % NS], (i / NS) & 1);
+        }
+    } else if (warp == NPW + 1) {
+        // ---------------------------------------------------------- MMA warp
+        constexpr uint32_t id = idesc_e4m3(128, TN);
+        int it = 0;
+        for (int t = tile0; t < p.tiles; t += tile_step)
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = it % NS, b = it & 1;
+                tcf::wait_warp(&full[s], (it / NS) & 1, abort_flag);
+                if (it >= 2) tcf::wait_warp(&acc_free[b], ((it >> 1) - 1) & 1, abort_flag);
+                __syncwarp();
+                tc::tc_after_sync();
+                if (tc::elect_one()) {
+                    const uint32_t la = tc::desc_lo(sbase + s * C::STAGE, 16),
+                                   lb = tc::desc_lo(sbase + s * C::STAGE + kLaneTile, 16);
+                    const uint32_t d = tmem + b * TN;
+                    mma_e4m3<0>(d, tc::desc(la), tc::desc(lb), id);
+#pragma unroll
+                    for (int k = 1; k < 4; ++k) mma_e4m3<1>(d, tc::desc(la + 2 * k), tc::desc(lb + 2 * k), id);
+                    tc::mma_commit(&empty[s]);
+                    tc::mma_commit(&acc_full[b]);
+                }
+                __syncwarp();
+            }
+        if (tc::elect_one()) {  // never leave with a product in flight
+            tc::mma_commit(drain);
+            tcf::drain_wait(drain, 0);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------- promotion warps
+        const int q = warp & 3;                    // lane quarter of tensor memory
+        const int c0 = CPT * (warp >> 2);          // first column of this thread
+        const int ln = 32 * q + lane;
+        const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + c0;
+        float* sc = reinterpret_cast<float*>(base + C::OFF_SC) + warp * 2 * CPT;
+        constexpr int NSC = TOKENS ? 1 : (CPT + 31) / 32;  // scales a lane fetches per block
+        int it = 0;
+        for (int t = tile0; t < p.tiles; t += tile_step) {
+            const int lrow = 128 * (t % p.tiles_l) + ln, crow = TN * (t / p.tiles_l) + c0;
+            float2 acc[CPT / 2];
+#pragma unroll
+            for (int j = 0; j < CPT / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+            // the scales of one block: tokens' by columns, or this lane's token's
+            auto fetch = [&](int kb, float (&v)[NSC]) {
+                const int nb = (TOKENS ? crow : lrow - lane) / 128;
+                const float w = 128 * nb < g.N ? __ldg(g.ws + (int64_t)nb * kb_all + kb) : 0.f;
+#pragma unroll
+                for (int i = 0; i < NSC; ++i) {
+                    const int m = TOKENS ? lrow : crow + lane + 32 * i;
+                    v[i] = (m < g.M && (TOKENS || lane + 32 * i < CPT))
+                               ? w * __ldg(g.as + (int64_t)m * kb_all + kb) : 0.f;
+                }
+            };
+            float nxt[NSC];
+            fetch(kb0, nxt);
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int b = it & 1;
+                const float s = nxt[0];
+                float* scb = sc + b * CPT;
+                if constexpr (!TOKENS) {
+#pragma unroll
+                    for (int i = 0; i < NSC; ++i)
+                        if (lane + 32 * i < CPT) scb[lane + 32 * i] = nxt[i];
+                    __syncwarp();
+                }
+                if (kb + 1 < kb1) fetch(kb + 1, nxt);
+                tcf::wait(&acc_full[b], (it >> 1) & 1, abort_flag);
+                __syncwarp();
+                tc::tc_after_sync();
+                constexpr int STEP = CPT < 32 ? 16 : 32;
+#pragma unroll
+                for (int j = 0; j < CPT; j += STEP) {
+                    float v[STEP];
+                    if constexpr (STEP == 32)
+                        tc::tmem_ld32(taddr + b * TN + j, v);
+                    else
+                        tc::tmem_ld16(taddr + b * TN + j, v);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < STEP; i += 2) {
+                        float2 f;
+                        if constexpr (TOKENS)
+                            f = make_float2(s, s);
+                        else
+                            f = *reinterpret_cast<const float2*>(&scb[j + i]);
+                        acc[(j + i) / 2] = __ffma2_rn(make_float2(v[i], v[i + 1]), f, acc[(j + i) / 2]);
+                    }
+                }
+                tc::tc_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&acc_free[b]);
+            }
+            TOut* out = static_cast<TOut*>(g.out);
+            if constexpr (TOKENS) {
+                if (lrow < g.M) {
+                    TOut* o = out + (int64_t)lrow * g.N + crow;
+                    constexpr int V = 16 / sizeof(TOut);
+                    if (g.N % V == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0) {
+#pragma unroll
+                        for (int j = 0; j < CPT; j += V)
+                            if (crow + j < g.N) {
+                                uint4 u;
+                                TOut* e = reinterpret_cast<TOut*>(&u);
+#pragma unroll
+                                for (int i = 0; i < V; ++i)
+                                    e[i] = from_f32<TOut>((i & 1) ? acc[(j + i) / 2].y : acc[(j + i) / 2].x);
+                                *reinterpret_cast<uint4*>(o + j) = u;
+                            }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < CPT; ++j)
+                            if (crow + j < g.N) o[j] = from_f32<TOut>((j & 1) ? acc[j / 2].y : acc[j / 2].x);
+                    }
+                }
+            } else if (split == 1) {
+                if (lrow < g.N) {
+#pragma unroll
+                    for (int j = 0; j < CPT; ++j)
+                        if (crow + j < g.M)
+                            out[(int64_t)(crow + j) * g.N + lrow] = from_f32<TOut>((j & 1) ? acc[j / 2].y : acc[j / 2].x);
+                }
+            } else {
+                // this CTA's part of the sums, [token][n], over the spent ring (one
+                // tile a cluster, every load and product of it done)
+                float* red = reinterpret_cast<float*>(base);
+#pragma unroll
+                for (int j = 0; j < CPT; ++j) red[(c0 + j) * 128 + ln] = (j & 1) ? acc[j / 2].y : acc[j / 2].x;
+            }
+        }
+    }
+    tc::tc_before_sync();
+    __syncthreads();
+    if constexpr (!TOKENS) {
+        if (split > 1) {
+            tc::cluster_sync();
+            const int n0 = 128 * (tile0 % p.tiles_l), m0 = TN * (tile0 / p.tiles_l);
+            const int toks = g.M - m0 < TN ? g.M - m0 : TN;
+            for (int e = rank * C::THREADS + threadIdx.x; e < toks * 128; e += split * C::THREADS) {
+                const int j = e >> 7, n = n0 + (e & 127);
+                float v = 0.f;
+                for (int r = 0; r < split; ++r) v += ld_cluster_f32(tc::mapa(sbase + 4 * e, (uint32_t)r));
+                if (n < g.N) static_cast<TOut*>(g.out)[(int64_t)(m0 + j) * g.N + n] = from_f32<TOut>(v);
+            }
+            tc::cluster_sync();  // no CTA leaves while another reads its sums
+        }
+    }
+    if (threadIdx.x == 0 && *abort_flag) record_status(GDN_ERR_TIMEOUT);
+    tc::tc_after_sync();
+    if (warp == 0) tc::tmem_dealloc(tmem, C::COLS);
+}
+
+// [rows, K] bytes, boxes of 128 bytes x box_rows rows; behind K and the rows, zeros.
+inline bool make_map8(CUtensorMap* m, const void* ptr, int64_t rows, int64_t K, int64_t ld, int box_rows) {
+    tcf::EncodeTiled enc = tcf::get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld};
+    cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool TOKENS, int TN, typename TOut>
+inline cudaError_t launch_tc(const Args& g, int split, int sms, cudaStream_t st) {
+    using C = Cfg<TOKENS, TN>;
+    TcArgs p;
+    memset(&p, 0, sizeof(p));
+    const bool ok = TOKENS ? make_map8(&p.lanes, g.a, g.M, g.K, g.lda, 128) &&
+                                 make_map8(&p.cols, g.w, g.N, g.K, g.ldw, TN)
+                           : make_map8(&p.lanes, g.w, g.N, g.K, g.ldw, 128) &&
+                                 make_map8(&p.cols, g.a, g.M, g.K, g.lda, TN);
+    if (!ok) return cudaErrorInvalidValue;
+    p.g = g;
+    const int64_t lanes = TOKENS ? g.M : g.N, cols = TOKENS ? g.N : g.M;
+    const int64_t tl = (lanes + 127) / 128, tiles = tl * ((cols + TN - 1) / TN);
+    if (tiles > 0x7fffffff / 8) return cudaErrorInvalidValue;
+    p.tiles_l = (int)tl;
+    p.tiles = (int)tiles;
+    p.split = split;
+    auto kern = fp8_matmul_tc_kernel<TOKENS, TN, TOut>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.blockDim = dim3(C::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : (tiles < sms ? tiles : sms)), 1, 1);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// The form and split for a size.
+template <typename TOut>
+inline cudaError_t launch_fp8_matmul(const Args& g, int sms, cudaStream_t st) {
+    const int64_t tok_tiles = (int64_t)((g.M + 127) / 128) * ((g.N + 255) / 256);
+    if (g.M > 128 && tok_tiles >= sms / 2) return launch_tc<true, 256, TOut>(g, 1, sms, st);
+    const int tn = g.M <= 16 ? 16 : (g.M <= 32 ? 32 : (g.M <= 64 ? 64 : 128));
+    const int64_t tiles = (int64_t)((g.N + 127) / 128) * ((g.M + tn - 1) / tn);
+    const int kb = (g.K + 127) / 128;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= sms && kb / (split * 2) >= 2) split *= 2;
+    if (tn == 16) return launch_tc<false, 16, TOut>(g, split, sms, st);
+    if (tn == 32) return launch_tc<false, 32, TOut>(g, split, sms, st);
+    if (tn == 64) return launch_tc<false, 64, TOut>(g, split, sms, st);
+    return launch_tc<false, 128, TOut>(g, split, sms, st);
+}
+
+}  // namespace mm8
+}  // namespace gdn

@@ -20,6 +20,7 @@
 #include "ssm_decode.cuh"
 #include "rmsnorm_fp8.cuh"
 #include "fp8_matmul.cuh"
+#include "fp8_matmul_tc.cuh"
 
 namespace {
 
@@ -806,6 +807,11 @@ gdn_status gdn_fp8_matmul(const void* a, int64_t a_stride, const float* a_scales
     const gdn::mm8::Args g{static_cast<const uint8_t*>(a), a_scales, static_cast<const uint8_t*>(w),
                            w_scales, a_stride, w_stride, (int)M, N, K, out};
     cudaStream_t st = as_stream(stream);
+    // TMA wants rows that start on 16 bytes; others take the plain kernel
+    if (aligned16(a) && aligned16(w) && a_stride % 16 == 0 && w_stride % 16 == 0)
+        return cuda_check(out_dtype == GDN_BF16
+                              ? gdn::mm8::launch_fp8_matmul<__nv_bfloat16>(g, num_sms(), st)
+                              : gdn::mm8::launch_fp8_matmul<float>(g, num_sms(), st));
     const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 63) / 64));
     if (out_dtype == GDN_BF16) gdn::mm8::fp8_matmul_simt_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(g);
     else gdn::mm8::fp8_matmul_simt_kernel<float><<<grid, 256, 0, st>>>(g);
