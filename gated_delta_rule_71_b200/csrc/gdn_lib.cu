@@ -17,6 +17,7 @@
 #include "conv1d.cuh"
 #include "decode_step.cuh"
 #include "ssm_scan.cuh"
+#include "ssm_scan_tc.cuh"
 #include "ssm_decode.cuh"
 #include "rmsnorm_fp8.cuh"
 #include "fp8_matmul.cuh"
@@ -672,8 +673,19 @@ extern "C" {
 
 size_t gdn_ssm_scan_workspace_size(int n_seq, int64_t T_total, int H, int G, int P, int N,
                                    gdn_dtype dtype) {
-    (void)n_seq; (void)T_total; (void)H; (void)G; (void)P; (void)N; (void)dtype;
-    return 0;
+    // room for the segment states of a long sequence cut up (packed lengths are not
+    // known here: the larger of the dense and the packed plan)
+    if (n_seq <= 0 || T_total <= 0 || H < 1 || G < 1 || H % G || !head_dim_ok(P) || !head_dim_ok(N) ||
+        dtype != GDN_BF16)
+        return 0;
+    size_t need = 0;
+    for (int packed = 0; packed < 2; ++packed) {
+        if (!packed && T_total % n_seq) continue;
+        const size_t b = gdn::ssm::scan_part_bytes(
+            gdn::ssm::plan_scan(n_seq, T_total, packed != 0, H, G, P, num_sms()), N);
+        if (b > need) need = b;
+    }
+    return need;
 }
 
 gdn_status gdn_ssm_scan(const void* x, int64_t x_stride, const void* dt, int64_t dt_stride,
@@ -712,7 +724,16 @@ gdn_status gdn_ssm_scan(const void* x, int64_t x_stride, const void* dt, int64_t
     gdn::ssm::ScanArgs a{x,    Bm,      Cm, dt, z,  x_stride,   b_stride, c_stride, dt_stride,
                          z_stride, A_log, dt_bias, D, h0, cu_seqlens, n_seq, T, H, G, P, N, y, hT};
     cudaStream_t st = as_stream(stream);
-    return dtype == GDN_BF16 ? launch_scan_simt<__nv_bfloat16>(a, st) : launch_scan_simt<float>(a, st);
+    if (dtype == GDN_F32) return launch_scan_simt<float>(a, st);
+    using gdn::ssm::tma_rows;
+    const gdn::ssm::ScanPlan r =
+        gdn::ssm::plan_scan(n_seq, rows, cu_seqlens != nullptr, H, G, P, num_sms());
+    // rows on 16 bytes (y is [rows, H, P] and needs the same) take the tensor cores
+    if (rows > 0 && rows < ((int64_t)1 << 31) && tma_rows(x, x_stride) && tma_rows(Bm, b_stride) &&
+        tma_rows(Cm, c_stride) && aligned16(y) && r.segments * r.units < 0x7fffffff &&
+        (r.slots == 0 || (n_seq <= 65535 && r.units <= 65535)))
+        return cuda_check(gdn::ssm::launch_scan_tc(a, rows, r, workspace, st));
+    return launch_scan_simt<__nv_bfloat16>(a, st);
 }
 
 size_t gdn_ssm_decode_step_workspace_size(int n, int H, int G, int P, int N) {

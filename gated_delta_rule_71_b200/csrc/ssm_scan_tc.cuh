@@ -1,0 +1,878 @@
+// ssm_scan_tc.cuh -- the selective state space scan on the tensor cores (bf16
+// rows that TMA can address; fp32 states).
+//
+// Chunks of 128 tokens.  With g_t = -exp(A_log) dt_t (<= 0), G the inclusive sum
+// of g over a chunk, R_s = sum of g behind s, and h the state entering the chunk:
+//     y_r = sum_{s <= r} (C_r . B_s) e^{G_r - G_s} dt_s x_s  +  e^{G_r} h^T C_r
+//     h  <- e^{G_last} h + sum_s B_s (e^{R_s} dt_s x_s)^T
+// Four products a chunk on tcgen05 (M = 128, fp32 accumulation):
+//   CB  = C B^T                     tokens x tokens, shared by the CTA's heads
+//   Y2  = C h                       h in bf16 from shared memory
+//   Y1  = W x                       W = the decayed, masked CB in bf16, in tensor
+//                                   memory in place of CB; x as it came
+//   S  += (w x)^T B                 S = h^T accumulates in tensor memory in fp32
+// The weights e^{R_s} dt_s are fp32, so w x is split into three bf16 terms (24
+// bits): states keep fp32 accuracy.  W and the copy of h that multiplies C are
+// rounded to bf16 once each, as y itself is.
+//
+// Decays are factored so that every exponent is <= 0 (nothing overflows) and is a
+// sum of same-signed terms or a difference within 32 tokens: for s in an earlier
+// block of 32 than r, e^{G_r - G_s} = rowfac(r, block) * colfac(s), one exponential
+// per row and block; inside a block it is taken per pair.
+//
+// A CTA owns 128 value lanes (two heads of 64 or 32 value columns of one group, or
+// one head of 128) of one segment of a sequence.  Twenty warps, each with one job:
+//   X (4)  reads x, writes the split (w x)^T to tensor memory, 32 tokens at a time
+//   M (4)  turns CB into W          S (4)  decays S, hands its bf16 copy to C h
+//   Y (4)  y = Y1 + e^G Y2 + D x, gate, store      gates (2), TMA (1), MMA (1)
+// The tensor pipe is the bound (N = 128: 3300 cycles of products a chunk); the MMA
+// warp orders the products so that each wait falls under another product.
+//
+// Long sequences with few heads are cut into segments: a first launch (STATES)
+// sums each segment's own contribution to the state, a small one chains them, and
+// the main launch starts each segment from the state that enters it.
+#pragma once
+
+#include "chunk_tc.cuh"
+#include "ssm_scan.cuh"
+
+namespace gdn {
+namespace ssm {
+
+constexpr int L = 128;          // tokens of a chunk
+constexpr int kScanThreads = 640;
+constexpr int NGR = 3;          // gate ring
+constexpr int NXB = 3;          // half-tiles of x in flight
+constexpr float kMinG2 = -160.f;  // 2^-160 is 0 in fp32: more decay changes nothing
+
+struct Gates {                  // of one chunk and head; sums in log2 units
+    float pre[L];               // inclusive sum within the token's block of 32
+    float col[L];               // dt 2^(sum behind the token within its block)
+    float w[L];                 // dt 2^(sum behind the token within the chunk)
+    float eG[L];                // 2^(inclusive sum within the chunk)
+    float dt[L];
+    float tot[4];               // block sums
+    float last;                 // 2^(sum of the chunk)
+    float lastg;                // the chunk's sum itself
+    float pad[2];
+};
+
+struct ScanTcArgs {
+    CUtensorMap x, b, c;        // (P, H, rows), (N, G, rows), boxes 64 x 1 x 128
+    ScanArgs a;
+    int pairs;                  // CTAs' worth of value lanes of a group
+    int units;                  // of all groups
+    int seg_chunks;             // chunks of a segment
+    float* part;                // [slots, units, N, 128] segment states
+    float* part_g;              // [slots, units, 2] segment sums of g (log2)
+};
+
+template <int NP>
+struct ScanCfg {
+    static constexpr int NH = NP / 64;
+    static constexpr uint32_t TILE = 16384;             // 128 rows of 128 bytes
+    static constexpr uint32_t BT = NH * TILE;
+    static constexpr uint32_t OFF_B = 0;                // [2]
+    static constexpr uint32_t OFF_C = OFF_B + 2 * BT;   // [2]
+    static constexpr uint32_t OFF_X = OFF_C + 2 * BT;   // [NXB]
+    static constexpr uint32_t OFF_H = OFF_X + NXB * TILE;
+    static constexpr uint32_t OFF_G = OFF_H + BT;       // [NGR][2] Gates
+    static constexpr uint32_t OFF_BAR = OFF_G + NGR * 2 * (uint32_t)sizeof(Gates);
+    static constexpr uint32_t SMEM = OFF_BAR + 48 * 8 + 64 + 1024;
+    static_assert(SMEM <= 232448, "shared memory budget");
+    // tensor memory columns
+    static constexpr uint32_t COL_CB = 0;               // fp32 CB, then W of both heads
+    static constexpr uint32_t COL_S = 128;              // S, lane = value lane, NP columns
+    static constexpr uint32_t COL_Y1 = COL_S + NP;
+    static constexpr uint32_t COL_Y2 = COL_Y1 + 64;
+    static constexpr uint32_t COL_WX = COL_Y2 + 64;     // [2] x 48: three terms of 32 tokens
+    static_assert(COL_WX + 96 <= 512, "tensor memory budget");
+};
+
+enum : int {
+    B_FULL = 0, B_FREE = 2, C_FULL_ = 4, C_FREE_ = 6, X_FULL = 8, X_FREE = 11, G_FULL = 14, G_FREE = 17,
+    CB_FULL = 20, M_FULL, W_FREE, XQ_FULL, XQ_FREE = XQ_FULL + 2, S_READY = XQ_FREE + 2, DS_DONE, H_FREE,
+    Y_FULL, Y_FREE, CLEAN, S_DRAIN, N_SCAN_BARS
+};
+static_assert(N_SCAN_BARS <= 48, "barrier slots");
+
+// 3-D tiled load of one box (x innermost), completing on `bar`.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ float ex2_approx(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// Segments of a sequence of `len` tokens: every one but the last is full.
+__device__ __forceinline__ int64_t seq_segments(int64_t len, int64_t seg) {
+    return len <= seg ? 1 : (len + seg - 1) / seg;
+}
+
+// Where segment k of the batch lies: its sequence, its place j in it, how many the
+// sequence has, and the first slot of the sequence's segment states (its segments
+// but the last, counted over the sequences before it).  STATES counts those
+// segments only.  Called by one whole warp; false when there is no segment k.
+struct Segment { int seq; int j; int n; int slot; };
+template <bool STATES>
+__device__ inline bool find_segment(const ScanArgs& a, int64_t k, int64_t seg, int lane, Segment& o) {
+    if (!a.cu) {
+        const int64_t n = seq_segments(a.T, seg), per = STATES ? n - 1 : n;
+        if (per == 0 || k >= per * a.n_seq) return false;
+        o.seq = (int)(k / per);
+        o.j = (int)(k - o.seq * per);
+        o.n = (int)n;
+        o.slot = (int)(o.seq * (n - 1));
+        return true;
+    }
+    int64_t before = 0, slots = 0;
+    for (int s0 = 0; s0 < a.n_seq; s0 += 32) {
+        const int s = s0 + lane;
+        const int64_t n = s < a.n_seq ? seq_segments((int64_t)a.cu[s + 1] - a.cu[s], seg) : 0;
+        const int64_t full = s < a.n_seq ? n - 1 : 0, own = STATES ? full : n;
+        int64_t inc = own, fin = full;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, inc, d), v = __shfl_up_sync(0xffffffffu, fin, d);
+            if (lane >= d) {
+                inc += u;
+                fin += v;
+            }
+        }
+        const int64_t first = before + inc - own;
+        const uint32_t hit = __ballot_sync(0xffffffffu, k >= first && k < first + own);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            o.seq = s0 + src;
+            o.j = (int)(k - __shfl_sync(0xffffffffu, first, src));
+            o.n = (int)__shfl_sync(0xffffffffu, n, src);
+            o.slot = (int)(slots + __shfl_sync(0xffffffffu, fin - full, src));
+            return true;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+        slots += __shfl_sync(0xffffffffu, fin, 31);
+    }
+    return false;
+}
+
+// The value lanes of a unit: half j is 64 lanes of one head.
+struct Half { int head; int col; int width; };  // width 0: no such head
+__device__ __forceinline__ Half half_of(const ScanTcArgs& p, int unit, int j) {
+    const int per = p.a.H / p.a.G, g = unit / p.pairs, u = unit - g * p.pairs;
+    if (p.a.P == 128) return Half{g * per + u, 64 * j, 64};
+    const int h = 2 * u + j;
+    return Half{g * per + h, 0, h < per ? p.a.P : 0};
+}
+
+// Grid: segments * units.
+template <int NP, bool STATES>
+__global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_constant__ ScanTcArgs p) {
+    using K = ScanCfg<NP>;
+    constexpr int NH = K::NH;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_u32 = smem_u32(smem_raw);
+    const uint32_t sbase = (raw_u32 + 1023u) & ~1023u;
+    uint8_t* base = smem_raw + (sbase - raw_u32);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(base + K::OFF_BAR);
+    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 48);
+    volatile uint32_t* abort_flag = misc + 1;
+    Gates* gates = reinterpret_cast<Gates*>(base + K::OFF_G);
+    const ScanArgs& a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int unit = blockIdx.x % p.units;
+    const int64_t seg_tokens = (int64_t)p.seg_chunks * L;
+    Segment sg;
+    if (!find_segment<STATES>(a, blockIdx.x / p.units, seg_tokens, lane, sg)) return;  // all warps alike
+    int64_t r0, r1;
+    seq_rows(a, sg.seq, r0, r1);
+    r0 += sg.j * seg_tokens;
+    if (r1 > r0 + seg_tokens) r1 = r0 + seg_tokens;
+    r0 = __shfl_sync(0xffffffffu, r0, 0);
+    const int rows = __shfl_sync(0xffffffffu, (int)(r1 - r0), 0);
+    const int nch = (int)__reduce_max_sync(0xffffffffu, (uint32_t)((rows + L - 1) / L));
+    const int tail = rows - (nch - 1) * L;  // rows of the last chunk
+    const int grp = unit / p.pairs;
+    const bool one_head = a.P == 128;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < N_SCAN_BARS; ++i) {
+            uint32_t n = 1;
+            if (i >= X_FREE && i < X_FREE + NXB) n = STATES ? 2 : 7;  // 2 X warps (, 4 Y warps, the product)
+            if (i >= G_FULL && i < G_FULL + NGR) n = 2;
+            if (i >= G_FREE && i < G_FREE + NGR) n = STATES ? 8 : 16;
+            if (i == M_FULL || i == XQ_FULL || i == XQ_FULL + 1 || i == S_READY || i == Y_FREE || i == CLEAN) n = 4;
+            mbar_init(&bars[i], n);
+        }
+        misc[1] = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) tc::tmem_alloc(&misc[0], 512);
+    tc::tc_before_sync();
+    __syncthreads();
+    tc::tc_after_sync();
+    const uint32_t tmem = __reduce_max_sync(0xffffffffu, misc[0]);
+    auto wait = [&](int b, int phase) { return tcf::wait(&bars[b], (uint32_t)phase & 1u, abort_flag); };
+    auto arrive = [&](int b) {  // one arrival a warp
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars[b]);
+    };
+
+    const int q = warp & 3, ln = 32 * q + lane;  // tensor-memory lane of the four-warp jobs
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
+
+    if (warp < 4) {
+        // =============================================================== X warps
+        const int j = ln >> 6, pc = ln & 63;   // half, value column within it
+        uint32_t off[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) off[t] = t * 128 + ((((uint32_t)pc >> 3) ^ t) << 4) + (pc & 7) * 2;
+        for (int c = 0; c < nch; ++c) {
+            const int gs = c % NGR, xi = 2 * c + j, xb = xi % NXB;
+            if (c == nch - 1 && tail < L) {
+                // rows behind the sequence's end belong to another one: x and B to zero
+                // (a zero weight would still carry a NaN through the products)
+                for (int h = 0; h < 2; ++h) wait(X_FULL + (2 * c + h) % NXB, (2 * c + h) / NXB);
+                wait(B_FULL + (c & 1), c >> 1);
+                if (ln >= tail) {
+                    const uint32_t row = (uint32_t)ln * 128u;
+                    for (int i = 0; i < 8; ++i) {
+                        for (int h = 0; h < 2; ++h)
+                            tc::st_shared_v4(sbase + K::OFF_X + ((2 * c + h) % NXB) * K::TILE + row + 16 * i, 0, 0, 0, 0);
+                        for (int h = 0; h < NH; ++h)
+                            tc::st_shared_v4(sbase + K::OFF_B + (c & 1) * K::BT + h * K::TILE + row + 16 * i, 0, 0, 0, 0);
+                    }
+                }
+                tc::fence_async_smem();
+                tc::named_bar(1, 128);
+                arrive(CLEAN);
+            }
+            wait(X_FULL + xb, xi / NXB);
+            wait(G_FULL + gs, c / NGR);
+            const Gates& G = gates[2 * gs + (one_head ? 0 : j)];
+            const uint8_t* xt = base + K::OFF_X + xb * K::TILE;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                const int it = 4 * c + k, buf = it & 1;
+                uint32_t hi[16], mi[16], lo[16];
+#pragma unroll
+                for (int t = 0; t < 32; t += 4) {
+                    const float4 w = *reinterpret_cast<const float4*>(&G.w[32 * k + t]);
+                    const float wv[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        const uint8_t* row = xt + (32 * k + t + i) / 8 * 1024;
+                        const float v0 = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
+                                        row + off[(t + i) & 7])) * wv[i];
+                        const float v1 = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
+                                        row + off[(t + i + 1) & 7])) * wv[i + 1];
+                        const int o = (t + i) / 2;
+                        hi[o] = tc::pack_bf16(v0, v1);
+                        const float a0 = v0 - bf16_lo(hi[o]), a1 = v1 - bf16_hi(hi[o]);
+                        mi[o] = tc::pack_bf16(a0, a1);
+                        lo[o] = tc::pack_bf16(a0 - bf16_lo(mi[o]), a1 - bf16_hi(mi[o]));
+                    }
+                }
+                if (it >= 2) wait(XQ_FREE + buf, (it >> 1) - 1);
+                __syncwarp();
+                tc::tc_after_sync();
+                const uint32_t col = lane_base + K::COL_WX + 48 * buf;
+                tc::tmem_st16(col, hi);
+                tc::tmem_st16(col + 16, mi);
+                tc::tmem_st16(col + 32, lo);
+                tc::tmem_wait_st();
+                tc::tc_before_sync();
+                arrive(XQ_FULL + buf);
+            }
+            arrive(X_FREE + xb);
+            arrive(G_FREE + gs);
+        }
+    } else if (warp < 8) {
+        // =============================================================== M warps
+        if constexpr (!STATES) {
+            const uint32_t zero[16] = {};
+            const int heads = one_head ? 1 : 2;
+            for (int c = 0; c < nch; ++c) {
+                const int gs = c % NGR;
+                wait(G_FULL + gs, c / NGR);
+                wait(CB_FULL, c);
+                __syncwarp();
+                tc::tc_after_sync();
+#pragma unroll 1
+                for (int jb = 0; jb < 4; ++jb) {
+                    const uint32_t col = lane_base + K::COL_CB + 32 * jb;
+                    if (jb > q) {  // above the diagonal
+                        tc::tmem_st16(col, zero);
+                        tc::tmem_st16(col + 16, zero);
+                        continue;
+                    }
+                    float v[32];
+                    tc::tmem_ld32(col, v);
+                    tc::tmem_wait_ld();
+#pragma unroll 1
+                    for (int h = 0; h < heads; ++h) {
+                        const Gates& G = gates[2 * gs + h];
+                        const float pr = G.pre[ln];
+                        uint32_t o[16];
+                        if (jb < q) {
+                            float e = pr;
+                            for (int b = jb + 1; b < q; ++b) e += G.tot[b];
+                            const float rf = ex2_approx(e);
+#pragma unroll
+                            for (int s = 0; s < 32; s += 4) {
+                                const float4 f = *reinterpret_cast<const float4*>(&G.col[32 * jb + s]);
+                                o[s / 2] = tc::pack_bf16(v[s] * (rf * f.x), v[s + 1] * (rf * f.y));
+                                o[s / 2 + 1] = tc::pack_bf16(v[s + 2] * (rf * f.z), v[s + 3] * (rf * f.w));
+                            }
+                        } else {
+#pragma unroll
+                            for (int s = 0; s < 32; s += 4) {
+                                const float4 f = *reinterpret_cast<const float4*>(&G.pre[32 * jb + s]);
+                                const float4 d = *reinterpret_cast<const float4*>(&G.dt[32 * jb + s]);
+                                const float e0 = s <= lane ? v[s] * (ex2_approx(pr - f.x) * d.x) : 0.f;
+                                const float e1 = s + 1 <= lane ? v[s + 1] * (ex2_approx(pr - f.y) * d.y) : 0.f;
+                                const float e2 = s + 2 <= lane ? v[s + 2] * (ex2_approx(pr - f.z) * d.z) : 0.f;
+                                const float e3 = s + 3 <= lane ? v[s + 3] * (ex2_approx(pr - f.w) * d.w) : 0.f;
+                                o[s / 2] = tc::pack_bf16(e0, e1);
+                                o[s / 2 + 1] = tc::pack_bf16(e2, e3);
+                            }
+                        }
+                        tc::tmem_st16(col + 16 * h, o);
+                    }
+                }
+                tc::tmem_wait_st();
+                tc::tc_before_sync();
+                arrive(M_FULL);
+                arrive(G_FREE + gs);
+            }
+        }
+    } else if (warp < 12) {
+        // =============================================================== S warps
+        const int j = ln >> 6, pc = ln & 63;
+        const Half hf = half_of(p, unit, j);
+        const bool live = pc < hf.width;
+        const int64_t hb = (((int64_t)sg.seq * a.H + hf.head) * a.N) * a.P + hf.col + pc;
+        // the state that enters the segment
+        const float* src = nullptr;
+        int64_t step = 0;
+        if (!STATES) {
+            if (sg.j > 0) {
+                src = p.part + ((int64_t)(sg.slot + sg.j - 1) * p.units + unit) * a.N * 128 + ln;
+                step = 128;
+            } else if (a.h0) {
+                src = a.h0 + hb;
+                step = a.P;
+            }
+        }
+#pragma unroll 1
+        for (int n0 = 0; n0 < NP; n0 += 16) {
+            uint32_t u[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                u[i] = (src && live && n0 + i < a.N) ? __float_as_uint(src[(int64_t)(n0 + i) * step]) : 0u;
+            tc::tmem_st16(lane_base + K::COL_S + n0, u);
+        }
+        tc::tmem_wait_st();
+        float sum_g = 0.f;
+        for (int c = 0; c < nch; ++c) {
+            const int gs = c % NGR;
+            wait(G_FULL + gs, c / NGR);
+            const Gates& G = gates[2 * gs + (one_head ? 0 : j)];
+            const float e = G.last;
+            sum_g += G.lastg;
+            if (c > 0) wait(DS_DONE, c - 1);
+            if (!STATES && c > 0) wait(H_FREE, c - 1);
+            __syncwarp();
+            tc::tc_after_sync();
+#pragma unroll 1
+            for (int n0 = 0; n0 < NP; n0 += 32) {
+                float v[32];
+                tc::tmem_ld32(lane_base + K::COL_S + n0, v);
+                tc::tmem_wait_ld();
+                if constexpr (!STATES)
+                    tc::store_half_row_bf16(sbase + K::OFF_H + (n0 / 64) * K::TILE, ln, (n0 / 32) & 1, v);
+                uint32_t u[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i] * e);
+                tc::tmem_st16(lane_base + K::COL_S + n0, u);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[16 + i] * e);
+                tc::tmem_st16(lane_base + K::COL_S + n0 + 16, u);
+            }
+            tc::tmem_wait_st();
+            tc::fence_async_smem();
+            tc::tc_before_sync();
+            arrive(S_READY);
+            arrive(G_FREE + gs);
+        }
+        // the state that leaves it
+        if (nch > 0) wait(DS_DONE, nch - 1);
+        __syncwarp();
+        tc::tc_after_sync();
+        float* dst = nullptr;
+        if (STATES) {
+            const int64_t at = (int64_t)(sg.slot + sg.j) * p.units + unit;
+            dst = p.part + at * a.N * 128 + ln;
+            step = 128;
+            if (pc == 0) p.part_g[at * 2 + j] = sum_g;
+        } else if (a.hT && sg.j == sg.n - 1 && live) {
+            dst = a.hT + hb;
+            step = a.P;
+        }
+#pragma unroll 1
+        for (int n0 = 0; n0 < NP; n0 += 32) {
+            float v[32];
+            tc::tmem_ld32(lane_base + K::COL_S + n0, v);
+            tc::tmem_wait_ld();
+            if (dst)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (n0 + i < a.N) dst[(int64_t)(n0 + i) * step] = v[i];
+        }
+    } else if (warp < 16) {
+        // =============================================================== Y warps
+        if constexpr (!STATES) {
+            using bf = __nv_bfloat16;
+            for (int c = 0; c < nch; ++c) {
+                const int gs = c % NGR;
+                const int64_t row = r0 + (int64_t)c * L + ln;
+                const bool in = (int64_t)c * L + ln < rows;
+                wait(G_FULL + gs, c / NGR);
+#pragma unroll 1
+                for (int j = 0; j < 2; ++j) {
+                    const Half hf = half_of(p, unit, j);
+                    const int xi = 2 * c + j, xb = xi % NXB;
+                    const float e = gates[2 * gs + (one_head ? 0 : j)].eG[ln];
+                    const float Dh = a.D && hf.width ? a.D[hf.head] : 0.f;
+                    bf* y = static_cast<bf*>(a.y) + (row * a.H + hf.head) * a.P + hf.col;
+                    const bf* z = static_cast<const bf*>(a.z) + row * a.zs + (int64_t)hf.head * a.P + hf.col;
+                    const bool zv = a.z && (a.zs % 8 == 0) && (reinterpret_cast<uintptr_t>(a.z) & 15u) == 0;
+                    uint4 zu[8];
+                    if (zv && in) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (8 * i < hf.width) zu[i] = __ldg(reinterpret_cast<const uint4*>(z) + i);
+                    }
+                    wait(X_FULL + xb, xi / NXB);
+                    wait(Y_FULL, xi);
+                    __syncwarp();
+                    tc::tc_after_sync();
+                    const uint32_t xrow = sbase + K::OFF_X + xb * K::TILE;
+#pragma unroll
+                    for (int n0 = 0; n0 < 64; n0 += 16) {
+                        float y1[16], y2[16];
+                        tc::tmem_ld16(lane_base + K::COL_Y1 + n0, y1);
+                        tc::tmem_ld16(lane_base + K::COL_Y2 + n0, y2);
+                        tc::tmem_wait_ld();
+                        if (in && n0 < hf.width) {
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const uint4 xv = tc::ld_shared_v4(xrow + tc::sw128_off(ln, n0 / 8 + u));
+                                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                                uint32_t zw[4] = {};
+                                if (zv) {
+                                    const uint4 t = zu[n0 / 8 + u];
+                                    zw[0] = t.x; zw[1] = t.y; zw[2] = t.z; zw[3] = t.w;
+                                } else if (a.z) {
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        zw[i] = (uint32_t)__bfloat16_as_ushort(z[n0 + 8 * u + 2 * i]) |
+                                                ((uint32_t)__bfloat16_as_ushort(z[n0 + 8 * u + 2 * i + 1]) << 16);
+                                }
+                                uint32_t ow[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const int k = 8 * u + 2 * i;
+                                    float a0 = fmaf(e, y2[k], y1[k]), a1 = fmaf(e, y2[k + 1], y1[k + 1]);
+                                    if (a.D) {
+                                        a0 = fmaf(Dh, bf16_lo(xw[i]), a0);
+                                        a1 = fmaf(Dh, bf16_hi(xw[i]), a1);
+                                    }
+                                    if (a.z) {
+                                        a0 *= conv_silu(bf16_lo(zw[i]));
+                                        a1 *= conv_silu(bf16_hi(zw[i]));
+                                    }
+                                    ow[i] = tc::pack_bf16(a0, a1);
+                                }
+                                *reinterpret_cast<uint4*>(y + n0 + 8 * u) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+                            }
+                        }
+                    }
+                    tc::tc_before_sync();
+                    arrive(Y_FREE);
+                    arrive(X_FREE + xb);
+                }
+                arrive(G_FREE + gs);
+            }
+        }
+    } else if (warp < 18) {
+        // ============================================================ gate warps
+        const int j = warp - 16;
+        const Half hf = half_of(p, unit, j);
+        const bool on = hf.width > 0 && !(one_head && j == 1);
+        const float A2 = on ? -expf(a.A_log[hf.head]) * tcf::kLog2e : 0.f;
+        const float bias = on ? a.dt_bias[hf.head] : 0.f;
+        const __nv_bfloat16* dtp = static_cast<const __nv_bfloat16*>(a.dt) + hf.head;
+        float raw[4];
+        auto fetch = [&](int c) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t t = (int64_t)c * L + 4 * lane + i;
+                raw[i] = on && t < rows ? __bfloat162float(dtp[(r0 + t) * a.dts]) : 0.f;
+            }
+        };
+        if (nch > 0) fetch(0);
+        for (int c = 0; c < nch; ++c) {
+            const int gs = c % NGR;
+            float d[4], g[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool in = on && c * (int64_t)L + 4 * lane + i < rows;
+                d[i] = in ? softplus_f32(raw[i] + bias) : 0.f;
+                // (written so that a NaN stays one)
+                g[i] = d[i] * A2;
+                g[i] = g[i] < kMinG2 ? kMinG2 : g[i];
+            }
+            if (c + 1 < nch) fetch(c + 1);
+            // inclusive sums within the block of 32 tokens (8 lanes), from the left
+            // and, of the tokens behind, from the right
+            const float sum = (g[0] + g[1]) + (g[2] + g[3]);
+            float left = sum, right = sum;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, left, o), v = __shfl_down_sync(0xffffffffu, right, o);
+                if ((lane & 7) >= o) left += u;
+                if ((lane & 7) + o < 8) right += v;
+            }
+            float before = __shfl_up_sync(0xffffffffu, left, 1), behind = __shfl_down_sync(0xffffffffu, right, 1);
+            if ((lane & 7) == 0) before = 0.f;
+            if ((lane & 7) == 7) behind = 0.f;
+            float tot[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tot[b] = __shfl_sync(0xffffffffu, left, 8 * b + 7);
+            const int blk = lane >> 3;
+            float earlier = 0.f, later = 0.f;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if (b < blk) earlier += tot[b];
+                if (b > blk) later += tot[b];
+            }
+            const float p0 = before + g[0], p1 = p0 + g[1], p2 = p1 + g[2], p3 = p2 + g[3];
+            const float s3 = behind, s2 = s3 + g[3], s1 = s2 + g[2], s0 = s1 + g[1];
+            if (c >= NGR) wait(G_FREE + gs, c / NGR - 1);
+            __syncwarp();
+            Gates& G = gates[2 * gs + j];
+            const int t = 4 * lane;
+            *reinterpret_cast<float4*>(&G.pre[t]) = make_float4(p0, p1, p2, p3);
+            *reinterpret_cast<float4*>(&G.dt[t]) = make_float4(d[0], d[1], d[2], d[3]);
+            *reinterpret_cast<float4*>(&G.col[t]) =
+                make_float4(d[0] * exp2f(s0), d[1] * exp2f(s1), d[2] * exp2f(s2), d[3] * exp2f(s3));
+            *reinterpret_cast<float4*>(&G.w[t]) =
+                make_float4(d[0] * exp2f(s0 + later), d[1] * exp2f(s1 + later), d[2] * exp2f(s2 + later),
+                            d[3] * exp2f(s3 + later));
+            *reinterpret_cast<float4*>(&G.eG[t]) =
+                make_float4(exp2f(p0 + earlier), exp2f(p1 + earlier), exp2f(p2 + earlier), exp2f(p3 + earlier));
+            if (lane < 4) G.tot[lane] = lane == 0 ? tot[0] : (lane == 1 ? tot[1] : (lane == 2 ? tot[2] : tot[3]));
+            if (lane == 4) {
+                const float all = (tot[0] + tot[1]) + (tot[2] + tot[3]);
+                G.lastg = all;
+                G.last = exp2f(all);
+            }
+            arrive(G_FULL + gs);
+        }
+    } else if (warp == 18) {
+        // ============================================================== TMA warp
+        if (lane == 0) {
+            Half hf[2] = {half_of(p, unit, 0), half_of(p, unit, 1)};
+            // a missing second head reads the first one's columns: nothing uses them
+            if (hf[1].width == 0) hf[1] = hf[0];
+            int done = 0;
+            for (int c = 0; c < nch && !*abort_flag; ++c) {
+                const int r = (int)(r0 + (int64_t)c * L), st = c & 1;
+                if (c >= 2 && !wait(B_FREE + st, (c >> 1) - 1)) break;
+                tc::mbar_arrive_expect_tx(&bars[B_FULL + st], K::BT);
+                for (int h = 0; h < NH; ++h)
+                    tma_load_3d(base + K::OFF_B + st * K::BT + h * K::TILE, &p.b, 64 * h, grp, r, &bars[B_FULL + st]);
+                if (!STATES) {
+                    if (c >= 2) wait(C_FREE_ + st, (c >> 1) - 1);
+                    tc::mbar_arrive_expect_tx(&bars[C_FULL_ + st], K::BT);
+                    for (int h = 0; h < NH; ++h)
+                        tma_load_3d(base + K::OFF_C + st * K::BT + h * K::TILE, &p.c, 64 * h, grp, r, &bars[C_FULL_ + st]);
+                }
+                for (int j = 0; j < 2; ++j) {
+                    const int xi = 2 * c + j, xb = xi % NXB;
+                    if (xi >= NXB) wait(X_FREE + xb, xi / NXB - 1);
+                    tc::mbar_arrive_expect_tx(&bars[X_FULL + xb], K::TILE);
+                    tma_load_3d(base + K::OFF_X + xb * K::TILE, &p.x, hf[j].col, hf[j].head, r, &bars[X_FULL + xb]);
+                }
+                done = c + 1;
+            }
+            // never leave with a copy in flight
+            for (int c = done >= 2 ? done - 2 : 0; c < done; ++c) {
+                tcf::drain_wait(&bars[B_FULL + (c & 1)], (c >> 1) & 1);
+                if (!STATES) tcf::drain_wait(&bars[C_FULL_ + (c & 1)], (c >> 1) & 1);
+            }
+            for (int i = 2 * done >= NXB ? 2 * done - NXB : 0; i < 2 * done; ++i)
+                tcf::drain_wait(&bars[X_FULL + i % NXB], (i / NXB) & 1);
+        }
+    } else {
+        // ============================================================== MMA warp
+        constexpr uint32_t idCB = tc::idesc_bf16(128, 128, 0, 0), idY2 = tc::idesc_bf16(128, 64, 0, 0),
+                           idY1 = tc::idesc_bf16(128, 64, 0, 1), idS = tc::idesc_bf16(128, NP, 0, 1);
+        auto ready = [&](int b, int phase) {
+            tcf::wait_warp(&bars[b], (uint32_t)phase & 1u, abort_flag);
+            __syncwarp();
+            tc::tc_after_sync();
+        };
+        // one quarter of S += (w x)^T B, 32 tokens
+        auto issue_s = [&](int c, int k) {
+            const int it = 4 * c + k, buf = it & 1;
+            ready(XQ_FULL + buf, it >> 1);
+            if (tc::elect_one()) {
+                const uint32_t lb = tc::desc_lo(sbase + K::OFF_B + (c & 1) * K::BT, K::TILE);
+#pragma unroll
+                for (int s = 0; s < 3; ++s)
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks)
+                        tc::mma_ts<1>(tmem + K::COL_S, tmem + K::COL_WX + 48 * buf + 16 * s + 8 * ks,
+                                      tc::desc(lb + 128 * (2 * k + ks)), idS);
+                tc::mma_commit(&bars[XQ_FREE + buf]);
+                if (k == 3) {
+                    tc::mma_commit(&bars[DS_DONE]);
+                    tc::mma_commit(&bars[B_FREE + (c & 1)]);
+                }
+            }
+            __syncwarp();
+        };
+        auto issue_y2 = [&](int c, int j) {
+            if (tc::elect_one()) {
+                const uint32_t lc = tc::desc_lo(sbase + K::OFF_C + (c & 1) * K::BT, 16),
+                               lh = tc::desc_lo(sbase + K::OFF_H + j * 8192, 16);
+                tc::mma_ss<0>(tmem + K::COL_Y2, tc::desc(lc), tc::desc(lh), idY2);
+#pragma unroll
+                for (int k = 1; k < NP / 16; ++k) {
+                    const uint32_t o = (k >> 2) * (K::TILE / 16) + (k & 3) * 2;
+                    tc::mma_ss<1>(tmem + K::COL_Y2, tc::desc(lc + o), tc::desc(lh + o), idY2);
+                }
+                if (j == 1) {
+                    tc::mma_commit(&bars[H_FREE]);
+                    tc::mma_commit(&bars[C_FREE_ + (c & 1)]);
+                }
+            }
+            __syncwarp();
+        };
+        auto issue_y1 = [&](int c, int j) {
+            const int xi = 2 * c + j, xb = xi % NXB;
+            ready(X_FULL + xb, xi / NXB);
+            if (tc::elect_one()) {
+                const uint32_t lx = tc::desc_lo(sbase + K::OFF_X + xb * K::TILE, K::TILE);
+                const uint32_t w = tmem + K::COL_CB + (one_head ? 0 : 16 * j);
+                tc::mma_ts<0>(tmem + K::COL_Y1, w, tc::desc(lx), idY1);
+#pragma unroll
+                for (int k = 1; k < 8; ++k)
+                    tc::mma_ts<1>(tmem + K::COL_Y1, w + 32 * (k >> 1) + 8 * (k & 1), tc::desc(lx + 128 * k), idY1);
+                tc::mma_commit(&bars[Y_FULL]);
+                tc::mma_commit(&bars[X_FREE + xb]);
+                if (j == 1) tc::mma_commit(&bars[W_FREE]);
+            }
+            __syncwarp();
+        };
+        for (int c = 0; c < nch; ++c) {
+            ready(B_FULL + (c & 1), c >> 1);
+            if (c == nch - 1 && tail < L) ready(CLEAN, 0);
+            if constexpr (STATES) {
+                ready(S_READY, c);
+                for (int k = 0; k < 4; ++k) issue_s(c, k);
+            } else {
+                ready(C_FULL_ + (c & 1), c >> 1);
+                if (c > 0) ready(W_FREE, c - 1);  // the last chunk's W has been read
+                if (tc::elect_one()) {
+                    const uint32_t lc = tc::desc_lo(sbase + K::OFF_C + (c & 1) * K::BT, 16),
+                                   lb = tc::desc_lo(sbase + K::OFF_B + (c & 1) * K::BT, 16);
+                    tc::mma_ss<0>(tmem + K::COL_CB, tc::desc(lc), tc::desc(lb), idCB);
+#pragma unroll
+                    for (int k = 1; k < NP / 16; ++k) {
+                        const uint32_t o = (k >> 2) * (K::TILE / 16) + (k & 3) * 2;
+                        tc::mma_ss<1>(tmem + K::COL_CB, tc::desc(lc + o), tc::desc(lb + o), idCB);
+                    }
+                    tc::mma_commit(&bars[CB_FULL]);
+                }
+                __syncwarp();
+                ready(S_READY, c);
+                if (c > 0) ready(Y_FREE, 2 * c - 1);
+                issue_y2(c, 0);
+                issue_s(c, 0);
+                issue_s(c, 1);
+                ready(M_FULL, c);
+                issue_y1(c, 0);
+                issue_s(c, 2);
+                issue_s(c, 3);
+                ready(Y_FREE, 2 * c);
+                issue_y2(c, 1);
+                issue_y1(c, 1);
+            }
+        }
+        if (tc::elect_one()) {  // never leave with a product in flight
+            tc::mma_commit(&bars[S_DRAIN]);
+            tcf::drain_wait(&bars[S_DRAIN], 0);
+        }
+        __syncwarp();
+    }
+    tc::tc_before_sync();
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) record_status(GDN_ERR_TIMEOUT);
+    tc::tc_after_sync();
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+// Chains the segment states of each sequence: slot j becomes the state behind
+// segment j.  Grid: (element blocks, units, sequences) of 256 threads.
+__global__ void __launch_bounds__(256) scan_chain_kernel(const __grid_constant__ ScanTcArgs p) {
+    const ScanArgs& a = p.a;
+    __shared__ int s_slot, s_n;
+    const int unit = blockIdx.y, seq = blockIdx.z;
+    const int64_t seg = (int64_t)p.seg_chunks * L;
+    if (threadIdx.x < 32) {
+        int64_t n, slot = 0;
+        if (!a.cu) {
+            n = seq_segments(a.T, seg);
+            slot = seq * (n - 1);
+        } else {
+            n = seq_segments((int64_t)a.cu[seq + 1] - a.cu[seq], seg);
+            if (n > 1)
+                for (int s = threadIdx.x; s < seq; s += 32) slot += seq_segments((int64_t)a.cu[s + 1] - a.cu[s], seg) - 1;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) slot += __shfl_xor_sync(0xffffffffu, slot, o);
+        }
+        if (threadIdx.x == 0) {
+            s_slot = (int)slot;
+            s_n = (int)n;
+        }
+    }
+    __syncthreads();
+    if (s_n < 2) return;
+    const int e = blockIdx.x * 256 + threadIdx.x;  // n * 128 + value lane
+    if (e >= a.N * 128) return;
+    const int n = e >> 7, ln = e & 127, j = ln >> 6;
+    const Half hf = half_of(p, unit, j);
+    float run = 0.f;
+    if (a.h0 && (ln & 63) < hf.width)
+        run = a.h0[(((int64_t)seq * a.H + hf.head) * a.N + n) * a.P + hf.col + (ln & 63)];
+    for (int i = 0; i + 1 < s_n; ++i) {
+        const int64_t at = (int64_t)(s_slot + i) * p.units + unit;
+        float* s = p.part + at * a.N * 128 + e;
+        run = fmaf(run, exp2f(p.part_g[at * 2 + (a.P == 128 ? 0 : j)]), *s);
+        *s = run;
+    }
+}
+
+// ------------------------------------------------------------------------ host
+
+inline bool make_map3(CUtensorMap* m, const void* ptr, int inner, int mid, int64_t rows, int64_t row_stride) {
+    tcf::EncodeTiled enc = tcf::get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)mid, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)inner * 2, (cuuint64_t)row_stride * 2};
+    cuuint32_t box[3] = {64u, 1u, (cuuint32_t)L};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct ScanPlan {
+    int pairs, units;
+    int seg_chunks;   // chunks of a segment
+    int64_t segments; // at most
+    int64_t slots;    // segment states: full segments that are not a sequence's last, at most
+};
+
+// How long the segments are.  One segment a sequence keeps the SMs busy when there
+// are many (sequence, unit) chains.  With fewer, cutting a sequence costs a first
+// pass over its products into the state (about half a chunk's time) for every
+// segment but the last, and shortens the walk: the cheapest of the cuts into whole
+// waves, in chunk times.
+inline ScanPlan plan_scan(int n_seq, int64_t T_total, bool packed, int H, int G, int P, int sms) {
+    ScanPlan r;
+    r.pairs = P == 128 ? H / G : (H / G + 1) / 2;
+    r.units = G * r.pairs;
+    const int64_t len = packed ? T_total : T_total / n_seq;
+    const int64_t chunks = (len + L - 1) / L;
+    double best = 0;
+    r.seg_chunks = 0x400000;
+    for (int cut = 1; cut <= 160 && (cut == 1 || cut * 4 <= chunks); ++cut) {
+        const int64_t sc = (chunks + cut - 1) / cut;
+        const int64_t nseg = chunks ? (chunks + sc - 1) / sc : 1;
+        // packed sequences end where they like: count a segment more for each
+        const int64_t main = (packed ? nseg + n_seq - 1 : n_seq * nseg) * r.units;
+        const int64_t first = (packed ? nseg - 1 : n_seq * (nseg - 1)) * r.units;
+        const double cost = (double)((main + sms - 1) / sms) * sc + 0.5 * (double)((first + sms - 1) / sms) * sc +
+                            (nseg > 1 ? 4.0 : 0.0);
+        if (cut == 1 || cost < best) {
+            best = cost;
+            r.seg_chunks = (int)(sc > 0 ? sc : 1);
+        }
+    }
+    const int64_t seg = (int64_t)r.seg_chunks * L;
+    if (packed) {
+        r.slots = T_total > seg ? T_total / seg : 0;
+        r.segments = r.slots + n_seq;
+    } else {
+        const int64_t n = len <= seg ? 1 : (len + seg - 1) / seg;
+        r.slots = (n - 1) * n_seq;
+        r.segments = n * n_seq;
+    }
+    return r;
+}
+
+inline size_t scan_part_bytes(const ScanPlan& r, int N) {
+    return ((size_t)r.slots * r.units * ((size_t)N * 128 + 2) * 4 + 255) / 256 * 256;
+}
+
+// Whether TMA can address the rows of t.
+inline bool tma_rows(const void* t, int64_t stride) {
+    return (reinterpret_cast<uintptr_t>(t) & 15u) == 0 && stride % 8 == 0;
+}
+
+template <int NP>
+inline cudaError_t launch_scan_np(const ScanTcArgs& p, const ScanPlan& r, cudaStream_t st) {
+    using K = ScanCfg<NP>;
+    cudaError_t e = cudaFuncSetAttribute(scan_tc_kernel<NP, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::SMEM);
+    if (e != cudaSuccess) return e;
+    if (r.slots > 0) {
+        e = cudaFuncSetAttribute(scan_tc_kernel<NP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::SMEM);
+        if (e != cudaSuccess) return e;
+        scan_tc_kernel<NP, true><<<(unsigned)(r.slots * r.units), kScanThreads, K::SMEM, st>>>(p);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        scan_chain_kernel<<<dim3((unsigned)(p.a.N / 2), (unsigned)r.units, (unsigned)p.a.n_seq), 256, 0, st>>>(p);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    scan_tc_kernel<NP, false><<<(unsigned)(r.segments * r.units), kScanThreads, K::SMEM, st>>>(p);
+    return cudaGetLastError();
+}
+
+inline cudaError_t launch_scan_tc(const ScanArgs& a, int64_t rows, const ScanPlan& r, void* workspace, cudaStream_t st) {
+    ScanTcArgs p;
+    memset(&p, 0, sizeof(p));
+    if (!make_map3(&p.x, a.x, a.P, a.H, rows, a.xs) || !make_map3(&p.b, a.Bm, a.N, a.G, rows, a.bs) ||
+        !make_map3(&p.c, a.Cm, a.N, a.G, rows, a.cs))
+        return cudaErrorInvalidValue;
+    p.a = a;
+    p.pairs = r.pairs;
+    p.units = r.units;
+    p.seg_chunks = r.seg_chunks;
+    p.part = static_cast<float*>(workspace);
+    p.part_g = p.part + r.slots * r.units * a.N * 128;
+    return a.N == 128 ? launch_scan_np<128>(p, r, st) : launch_scan_np<64>(p, r, st);
+}
+
+}  // namespace ssm
+}  // namespace gdn
