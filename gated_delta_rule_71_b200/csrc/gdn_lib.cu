@@ -730,7 +730,7 @@ gdn_status gdn_ssm_scan(const void* x, int64_t x_stride, const void* dt, int64_t
         gdn::ssm::plan_scan(n_seq, rows, cu_seqlens != nullptr, H, G, P, num_sms());
     // rows on 16 bytes (y is [rows, H, P] and needs the same) take the tensor cores
     if (rows > 0 && rows < ((int64_t)1 << 31) && tma_rows(x, x_stride) && tma_rows(Bm, b_stride) &&
-        tma_rows(Cm, c_stride) && aligned16(y) && r.segments * r.units < 0x7fffffff &&
+        tma_rows(Cm, c_stride) && (!z || tma_rows(z, z_stride)) && aligned16(y) && r.segments * r.units < 0x7fffffff &&
         (r.slots == 0 || (n_seq <= 65535 && r.units <= 65535)))
         return cuda_check(gdn::ssm::launch_scan_tc(a, rows, r, workspace, st));
     return launch_scan_simt<__nv_bfloat16>(a, st);

@@ -40,9 +40,9 @@ namespace gdn {
 namespace ssm {
 
 constexpr int L = 128;          // tokens of a chunk
-constexpr int kScanThreads = 640;
+constexpr int kScanThreads = 896;
 constexpr int NGR = 3;          // gate ring
-constexpr int NXB = 3;          // half-tiles of x in flight
+constexpr int NXB = 5;           // half-tiles of x in flight (then of z, then of y)
 constexpr float kMinG2 = -160.f;  // 2^-160 is 0 in fp32: more decay changes nothing
 
 struct Gates {                  // of one chunk and head; sums in log2 units
@@ -50,7 +50,7 @@ struct Gates {                  // of one chunk and head; sums in log2 units
     float col[L];               // dt 2^(sum behind the token within its block)
     float w[L];                 // dt 2^(sum behind the token within the chunk)
     float eG[L];                // 2^(inclusive sum within the chunk)
-    float dt[L];
+    float prd[L];               // log2(dt) - pre
     float tot[4];               // block sums
     float last;                 // 2^(sum of the chunk)
     float lastg;                // the chunk's sum itself
@@ -58,7 +58,7 @@ struct Gates {                  // of one chunk and head; sums in log2 units
 };
 
 struct ScanTcArgs {
-    CUtensorMap x, b, c;        // (P, H, rows), (N, G, rows), boxes 64 x 1 x 128
+    CUtensorMap x, b, c, z, y;  // (P, H, rows), (N, G, rows), boxes 64 x 1 x 128
     ScanArgs a;
     int pairs;                  // CTAs' worth of value lanes of a group
     int units;                  // of all groups
@@ -73,28 +73,28 @@ struct ScanCfg {
     static constexpr uint32_t TILE = 16384;             // 128 rows of 128 bytes
     static constexpr uint32_t BT = NH * TILE;
     static constexpr uint32_t OFF_B = 0;                // [2]
-    static constexpr uint32_t OFF_C = OFF_B + 2 * BT;   // [2]
-    static constexpr uint32_t OFF_X = OFF_C + 2 * BT;   // [NXB]
+    static constexpr uint32_t OFF_C = OFF_B + 2 * BT;
+    static constexpr uint32_t OFF_X = OFF_C + BT;       // [NXB]
     static constexpr uint32_t OFF_H = OFF_X + NXB * TILE;
     static constexpr uint32_t OFF_G = OFF_H + BT;       // [NGR][2] Gates
     static constexpr uint32_t OFF_BAR = OFF_G + NGR * 2 * (uint32_t)sizeof(Gates);
-    static constexpr uint32_t SMEM = OFF_BAR + 48 * 8 + 64 + 1024;
+    static constexpr uint32_t SMEM = OFF_BAR + 52 * 8 + 16 + 1024;
     static_assert(SMEM <= 232448, "shared memory budget");
     // tensor memory columns
     static constexpr uint32_t COL_CB = 0;               // fp32 CB, then W of both heads
     static constexpr uint32_t COL_S = 128;              // S, lane = value lane, NP columns
-    static constexpr uint32_t COL_Y1 = COL_S + NP;
-    static constexpr uint32_t COL_Y2 = COL_Y1 + 64;
-    static constexpr uint32_t COL_WX = COL_Y2 + 64;     // [2] x 48: three terms of 32 tokens
+    static constexpr uint32_t COL_Y = COL_S + NP;       // [2 halves] x 64: Y1, then Y2
+    static constexpr uint32_t COL_WX = COL_Y + 128;     // [2] x 48: three terms of 32 tokens
     static_assert(COL_WX + 96 <= 512, "tensor memory budget");
 };
 
 enum : int {
-    B_FULL = 0, B_FREE = 2, C_FULL_ = 4, C_FREE_ = 6, X_FULL = 8, X_FREE = 11, G_FULL = 14, G_FREE = 17,
-    CB_FULL = 20, M_FULL, W_FREE, XQ_FULL, XQ_FREE = XQ_FULL + 2, S_READY = XQ_FREE + 2, DS_DONE, H_FREE,
-    Y_FULL, Y_FREE, CLEAN, S_DRAIN, N_SCAN_BARS
+    B_FULL = 0, B_FREE = B_FULL + 2, C_FULL_ = B_FREE + 2, C_FREE_, X_FULL, X_DONE = X_FULL + NXB,
+    Z_FULL = X_DONE + NXB, X_FREE = Z_FULL + NXB, G_FULL = X_FREE + NXB, G_FREE = G_FULL + NGR,
+    CB_FULL = G_FREE + NGR, M_FULL, W_FREE, XQ_FULL, XQ_FREE = XQ_FULL + 2, S_READY = XQ_FREE + 2, DS_DONE,
+    H_FREE, Y_FULL, Y_FREE = Y_FULL + 2, CLEAN = Y_FREE + 2, S_DRAIN, N_SCAN_BARS
 };
-static_assert(N_SCAN_BARS <= 48, "barrier slots");
+static_assert(N_SCAN_BARS <= 52, "barrier slots");
 
 // 3-D tiled load of one box (x innermost), completing on `bar`.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
@@ -105,10 +105,29 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
+// Bounded wait for what is still in flight on the way out (no abort flag).
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t phase) {
+    const uint32_t at = smem_u32(bar);
+#pragma unroll 1
+    for (uint32_t i = 0; i < tcf::kPolls && !mbar_try_wait(at, phase); ++i) {
+    }
+}
 __device__ __forceinline__ float ex2_approx(float v) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
 }
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
@@ -183,7 +202,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     const uint32_t sbase = (raw_u32 + 1023u) & ~1023u;
     uint8_t* base = smem_raw + (sbase - raw_u32);
     uint64_t* bars = reinterpret_cast<uint64_t*>(base + K::OFF_BAR);
-    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 48);
+    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 52);
     volatile uint32_t* abort_flag = misc + 1;
     Gates* gates = reinterpret_cast<Gates*>(base + K::OFF_G);
     const ScanArgs& a = p.a;
@@ -206,10 +225,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     if (threadIdx.x == 0) {
         for (int i = 0; i < N_SCAN_BARS; ++i) {
             uint32_t n = 1;
-            if (i >= X_FREE && i < X_FREE + NXB) n = STATES ? 2 : 7;  // 2 X warps (, 4 Y warps, the product)
+            if (i >= X_DONE && i < X_DONE + NXB) n = STATES ? 4 : 9;  // X warps (, Y warps, the product)
             if (i >= G_FULL && i < G_FULL + NGR) n = 2;
-            if (i >= G_FREE && i < G_FREE + NGR) n = STATES ? 8 : 16;
-            if (i == M_FULL || i == XQ_FULL || i == XQ_FULL + 1 || i == S_READY || i == Y_FREE || i == CLEAN) n = 4;
+            if (i >= G_FREE && i < G_FREE + NGR) n = STATES ? 12 : 24;
+            if (i == M_FULL || i == XQ_FULL || i == XQ_FULL + 1 || i == S_READY || i == Y_FREE ||
+                i == Y_FREE + 1 || i == CLEAN)
+                n = 4;
             mbar_init(&bars[i], n);
         }
         misc[1] = 0u;
@@ -229,74 +250,83 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     const int q = warp & 3, ln = 32 * q + lane;  // tensor-memory lane of the four-warp jobs
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
 
-    if (warp < 4) {
+    if (warp < 8) {
         // =============================================================== X warps
+        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        // warpgroup k & 1 takes the quarters k and k + 2 of a chunk, through its own
+        // buffer of tensor memory
+        const int set = warp >> 2;
         const int j = ln >> 6, pc = ln & 63;   // half, value column within it
         uint32_t off[8];
 #pragma unroll
         for (int t = 0; t < 8; ++t) off[t] = t * 128 + ((((uint32_t)pc >> 3) ^ t) << 4) + (pc & 7) * 2;
+        const uint32_t col = lane_base + K::COL_WX + 48 * set;
         for (int c = 0; c < nch; ++c) {
             const int gs = c % NGR, xi = 2 * c + j, xb = xi % NXB;
             if (c == nch - 1 && tail < L) {
                 // rows behind the sequence's end belong to another one: x and B to zero
                 // (a zero weight would still carry a NaN through the products)
-                for (int h = 0; h < 2; ++h) wait(X_FULL + (2 * c + h) % NXB, (2 * c + h) / NXB);
-                wait(B_FULL + (c & 1), c >> 1);
-                if (ln >= tail) {
-                    const uint32_t row = (uint32_t)ln * 128u;
-                    for (int i = 0; i < 8; ++i) {
-                        for (int h = 0; h < 2; ++h)
-                            tc::st_shared_v4(sbase + K::OFF_X + ((2 * c + h) % NXB) * K::TILE + row + 16 * i, 0, 0, 0, 0);
-                        for (int h = 0; h < NH; ++h)
-                            tc::st_shared_v4(sbase + K::OFF_B + (c & 1) * K::BT + h * K::TILE + row + 16 * i, 0, 0, 0, 0);
+                if (set == 0) {
+                    for (int h = 0; h < 2; ++h) wait(X_FULL + (2 * c + h) % NXB, (2 * c + h) / NXB);
+                    wait(B_FULL + (c & 1), c >> 1);
+                    if (ln >= tail) {
+                        const uint32_t row = (uint32_t)ln * 128u;
+                        for (int i = 0; i < 8; ++i) {
+                            for (int h = 0; h < 2; ++h)
+                                tc::st_shared_v4(sbase + K::OFF_X + ((2 * c + h) % NXB) * K::TILE + row + 16 * i, 0, 0, 0, 0);
+                            for (int h = 0; h < NH; ++h)
+                                tc::st_shared_v4(sbase + K::OFF_B + (c & 1) * K::BT + h * K::TILE + row + 16 * i, 0, 0, 0, 0);
+                        }
                     }
+                    tc::fence_async_smem();
                 }
-                tc::fence_async_smem();
-                tc::named_bar(1, 128);
-                arrive(CLEAN);
+                tc::named_bar(1, 256);
+                if (set == 0) arrive(CLEAN);
             }
             wait(X_FULL + xb, xi / NXB);
             wait(G_FULL + gs, c / NGR);
-            const Gates& G = gates[2 * gs + (one_head ? 0 : j)];
-            const uint8_t* xt = base + K::OFF_X + xb * K::TILE;
+            const float* w = gates[2 * gs + (one_head ? 0 : j)].w + 32 * set;
+            const uint8_t* xt = base + K::OFF_X + xb * K::TILE + 4096 * set;
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-                const int it = 4 * c + k, buf = it & 1;
-                uint32_t hi[16], mi[16], lo[16];
+            for (int k = 0; k < 4; ++k) {  // 16 tokens: 32 set + 64 (k / 2) + 16 (k % 2)
+                const int t0 = 64 * (k >> 1) + 16 * (k & 1);
+                const uint8_t* rows8 = xt + t0 * 128;
+                uint32_t hi[8], mi[8], lo[8];
 #pragma unroll
-                for (int t = 0; t < 32; t += 4) {
-                    const float4 w = *reinterpret_cast<const float4*>(&G.w[32 * k + t]);
-                    const float wv[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int i = 0; i < 4; i += 2) {
-                        const uint8_t* row = xt + (32 * k + t + i) / 8 * 1024;
-                        const float v0 = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
-                                        row + off[(t + i) & 7])) * wv[i];
-                        const float v1 = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
-                                        row + off[(t + i + 1) & 7])) * wv[i + 1];
-                        const int o = (t + i) / 2;
-                        hi[o] = tc::pack_bf16(v0, v1);
-                        const float a0 = v0 - bf16_lo(hi[o]), a1 = v1 - bf16_hi(hi[o]);
-                        mi[o] = tc::pack_bf16(a0, a1);
-                        lo[o] = tc::pack_bf16(a0 - bf16_lo(mi[o]), a1 - bf16_hi(mi[o]));
-                    }
+                for (int t = 0; t < 16; t += 2) {
+                    const float2 wv = *reinterpret_cast<const float2*>(&w[t0 + t]);
+                    const uint8_t* row = rows8 + (t >> 3) * 1024;
+                    const uint32_t x0 = *reinterpret_cast<const uint16_t*>(row + off[t & 7]),
+                                   x1 = *reinterpret_cast<const uint16_t*>(row + off[(t + 1) & 7]);
+                    // 24 bits in three truncated terms of 8: the last is exact
+                    const float2 v = __fmul2_rn(make_float2(bf16_lo(x0), bf16_lo(x1)), wv);
+                    const float2 m = __fadd2_rn(v, make_float2(-bf16_hi(__float_as_uint(v.x)), -bf16_hi(__float_as_uint(v.y))));
+                    const float2 l = __fadd2_rn(m, make_float2(-bf16_hi(__float_as_uint(m.x)), -bf16_hi(__float_as_uint(m.y))));
+                    hi[t / 2] = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
+                    mi[t / 2] = __byte_perm(__float_as_uint(m.x), __float_as_uint(m.y), 0x7632);
+                    lo[t / 2] = __byte_perm(__float_as_uint(l.x), __float_as_uint(l.y), 0x7632);
                 }
-                if (it >= 2) wait(XQ_FREE + buf, (it >> 1) - 1);
-                __syncwarp();
-                tc::tc_after_sync();
-                const uint32_t col = lane_base + K::COL_WX + 48 * buf;
-                tc::tmem_st16(col, hi);
-                tc::tmem_st16(col + 16, mi);
-                tc::tmem_st16(col + 32, lo);
-                tc::tmem_wait_st();
-                tc::tc_before_sync();
-                arrive(XQ_FULL + buf);
+                const int use = 2 * c + (k >> 1);  // of this buffer
+                if ((k & 1) == 0) {
+                    if (use > 0) wait(XQ_FREE + set, use - 1);
+                    __syncwarp();
+                    tc::tc_after_sync();
+                }
+                tc::tmem_st8(col + 8 * (k & 1), hi);
+                tc::tmem_st8(col + 16 + 8 * (k & 1), mi);
+                tc::tmem_st8(col + 32 + 8 * (k & 1), lo);
+                if (k & 1) {
+                    tc::tmem_wait_st();
+                    tc::tc_before_sync();
+                    arrive(XQ_FULL + set);
+                }
             }
-            arrive(X_FREE + xb);
+            arrive(X_DONE + xb);
             arrive(G_FREE + gs);
         }
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         // =============================================================== M warps
+        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if constexpr (!STATES) {
             const uint32_t zero[16] = {};
             const int heads = one_head ? 1 : 2;
@@ -321,31 +351,38 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                     for (int h = 0; h < heads; ++h) {
                         const Gates& G = gates[2 * gs + h];
                         const float pr = G.pre[ln];
-                        uint32_t o[16];
                         if (jb < q) {
                             float e = pr;
                             for (int b = jb + 1; b < q; ++b) e += G.tot[b];
                             const float rf = ex2_approx(e);
 #pragma unroll
-                            for (int s = 0; s < 32; s += 4) {
-                                const float4 f = *reinterpret_cast<const float4*>(&G.col[32 * jb + s]);
-                                o[s / 2] = tc::pack_bf16(v[s] * (rf * f.x), v[s + 1] * (rf * f.y));
-                                o[s / 2 + 1] = tc::pack_bf16(v[s + 2] * (rf * f.z), v[s + 3] * (rf * f.w));
+                            for (int s0 = 0; s0 < 32; s0 += 16) {
+                                uint32_t o[8];
+#pragma unroll
+                                for (int s = 0; s < 16; s += 2) {
+                                    const float2 f = *reinterpret_cast<const float2*>(&G.col[32 * jb + s0 + s]);
+                                    const float2 m = __fmul2_rn(make_float2(v[s0 + s], v[s0 + s + 1]),
+                                                                __fmul2_rn(make_float2(rf, rf), f));
+                                    o[s / 2] = tc::pack_bf16(m.x, m.y);
+                                }
+                                tc::tmem_st8(col + 16 * h + s0 / 2, o);
                             }
                         } else {
 #pragma unroll
-                            for (int s = 0; s < 32; s += 4) {
-                                const float4 f = *reinterpret_cast<const float4*>(&G.pre[32 * jb + s]);
-                                const float4 d = *reinterpret_cast<const float4*>(&G.dt[32 * jb + s]);
-                                const float e0 = s <= lane ? v[s] * (ex2_approx(pr - f.x) * d.x) : 0.f;
-                                const float e1 = s + 1 <= lane ? v[s + 1] * (ex2_approx(pr - f.y) * d.y) : 0.f;
-                                const float e2 = s + 2 <= lane ? v[s + 2] * (ex2_approx(pr - f.z) * d.z) : 0.f;
-                                const float e3 = s + 3 <= lane ? v[s + 3] * (ex2_approx(pr - f.w) * d.w) : 0.f;
-                                o[s / 2] = tc::pack_bf16(e0, e1);
-                                o[s / 2 + 1] = tc::pack_bf16(e2, e3);
+                            for (int s0 = 0; s0 < 32; s0 += 16) {
+                                uint32_t o[8];
+#pragma unroll
+                                for (int s = 0; s < 16; s += 2) {
+                                    // 2^(pre_r - pre_s) dt_s with dt in the exponent
+                                    const float2 f = *reinterpret_cast<const float2*>(&G.prd[32 * jb + s0 + s]);
+                                    const float2 d = __fadd2_rn(make_float2(pr, pr), f);
+                                    const float2 m = __fmul2_rn(make_float2(v[s0 + s], v[s0 + s + 1]),
+                                                                make_float2(ex2_approx(d.x), ex2_approx(d.y)));
+                                    o[s / 2] = tc::pack_bf16(s0 + s <= lane ? m.x : 0.f, s0 + s + 1 <= lane ? m.y : 0.f);
+                                }
+                                tc::tmem_st8(col + 16 * h + s0 / 2, o);
                             }
                         }
-                        tc::tmem_st16(col + 16 * h, o);
                     }
                 }
                 tc::tmem_wait_st();
@@ -354,8 +391,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 arrive(G_FREE + gs);
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // =============================================================== S warps
+        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int j = ln >> 6, pc = ln & 63;
         const Half hf = half_of(p, unit, j);
         const bool live = pc < hf.width;
@@ -399,13 +437,17 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 tc::tmem_wait_ld();
                 if constexpr (!STATES)
                     tc::store_half_row_bf16(sbase + K::OFF_H + (n0 / 64) * K::TILE, ln, (n0 / 32) & 1, v);
-                uint32_t u[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i] * e);
-                tc::tmem_st16(lane_base + K::COL_S + n0, u);
+                for (int s = 0; s < 32; s += 8) {
+                    uint32_t u[8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[16 + i] * e);
-                tc::tmem_st16(lane_base + K::COL_S + n0 + 16, u);
+                    for (int i = 0; i < 8; i += 2) {
+                        const float2 m = __fmul2_rn(make_float2(v[s + i], v[s + i + 1]), make_float2(e, e));
+                        u[i] = __float_as_uint(m.x);
+                        u[i + 1] = __float_as_uint(m.y);
+                    }
+                    tc::tmem_st8(lane_base + K::COL_S + n0 + s, u);
+                }
             }
             tc::tmem_wait_st();
             tc::fence_async_smem();
@@ -437,85 +479,117 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 for (int i = 0; i < 32; ++i)
                     if (n0 + i < a.N) dst[(int64_t)(n0 + i) * step] = v[i];
         }
-    } else if (warp < 16) {
+    } else if (warp < 24) {
         // =============================================================== Y warps
+        if constexpr (!STATES) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        // warpgroup j: half j, one token a thread
         if constexpr (!STATES) {
             using bf = __nv_bfloat16;
+            const int j = (warp >> 2) & 1;
+            const Half hf = half_of(p, unit, j);
+            const float2 Dh = make_float2(a.D && hf.width ? a.D[hf.head] : 0.f, a.D && hf.width ? a.D[hf.head] : 0.f);
+            const uint32_t ycol = lane_base + K::COL_Y + 64 * j;
+            const bool first = (warp & 3) == 0 && lane == 0;
             for (int c = 0; c < nch; ++c) {
-                const int gs = c % NGR;
-                const int64_t row = r0 + (int64_t)c * L + ln;
-                const bool in = (int64_t)c * L + ln < rows;
-                wait(G_FULL + gs, c / NGR);
-#pragma unroll 1
-                for (int j = 0; j < 2; ++j) {
-                    const Half hf = half_of(p, unit, j);
-                    const int xi = 2 * c + j, xb = xi % NXB;
-                    const float e = gates[2 * gs + (one_head ? 0 : j)].eG[ln];
-                    const float Dh = a.D && hf.width ? a.D[hf.head] : 0.f;
-                    bf* y = static_cast<bf*>(a.y) + (row * a.H + hf.head) * a.P + hf.col;
-                    const bf* z = static_cast<const bf*>(a.z) + row * a.zs + (int64_t)hf.head * a.P + hf.col;
-                    const bool zv = a.z && (a.zs % 8 == 0) && (reinterpret_cast<uintptr_t>(a.z) & 15u) == 0;
-                    uint4 zu[8];
-                    if (zv && in) {
+                const int gs = c % NGR, xi = 2 * c + j, xb = xi % NXB;
+                const int row = (int)r0 + c * L;
+                float2 t[32];
+                wait(X_FULL + xb, xi / NXB);
+                if (first && a.z && hf.width) tma_prefetch_3d(&p.z, hf.col, hf.head, row);
+                const uint32_t xrow = sbase + K::OFF_X + xb * K::TILE;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (8 * i < hf.width) zu[i] = __ldg(reinterpret_cast<const uint4*>(z) + i);
+                for (int u = 0; u < 8; ++u) {
+                    if (a.D) {
+                        const uint4 xv = tc::ld_shared_v4(xrow + tc::sw128_off(ln, u));
+                        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            t[4 * u + i] = __fmul2_rn(Dh, make_float2(bf16_lo(xw[i]), bf16_hi(xw[i])));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) t[4 * u + i] = make_float2(0.f, 0.f);
                     }
-                    wait(X_FULL + xb, xi / NXB);
-                    wait(Y_FULL, xi);
-                    __syncwarp();
-                    tc::tc_after_sync();
-                    const uint32_t xrow = sbase + K::OFF_X + xb * K::TILE;
-#pragma unroll
-                    for (int n0 = 0; n0 < 64; n0 += 16) {
-                        float y1[16], y2[16];
-                        tc::tmem_ld16(lane_base + K::COL_Y1 + n0, y1);
-                        tc::tmem_ld16(lane_base + K::COL_Y2 + n0, y2);
-                        tc::tmem_wait_ld();
-                        if (in && n0 < hf.width) {
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const uint4 xv = tc::ld_shared_v4(xrow + tc::sw128_off(ln, n0 / 8 + u));
-                                const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-                                uint32_t zw[4] = {};
-                                if (zv) {
-                                    const uint4 t = zu[n0 / 8 + u];
-                                    zw[0] = t.x; zw[1] = t.y; zw[2] = t.z; zw[3] = t.w;
-                                } else if (a.z) {
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        zw[i] = (uint32_t)__bfloat16_as_ushort(z[n0 + 8 * u + 2 * i]) |
-                                                ((uint32_t)__bfloat16_as_ushort(z[n0 + 8 * u + 2 * i + 1]) << 16);
-                                }
-                                uint32_t ow[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const int k = 8 * u + 2 * i;
-                                    float a0 = fmaf(e, y2[k], y1[k]), a1 = fmaf(e, y2[k + 1], y1[k + 1]);
-                                    if (a.D) {
-                                        a0 = fmaf(Dh, bf16_lo(xw[i]), a0);
-                                        a1 = fmaf(Dh, bf16_hi(xw[i]), a1);
-                                    }
-                                    if (a.z) {
-                                        a0 *= conv_silu(bf16_lo(zw[i]));
-                                        a1 *= conv_silu(bf16_hi(zw[i]));
-                                    }
-                                    ow[i] = tc::pack_bf16(a0, a1);
-                                }
-                                *reinterpret_cast<uint4*>(y + n0 + 8 * u) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-                            }
-                        }
-                    }
-                    tc::tc_before_sync();
-                    arrive(Y_FREE);
-                    arrive(X_FREE + xb);
                 }
+                arrive(X_DONE + xb);
+                wait(G_FULL + gs, c / NGR);
+                const float eg = gates[2 * gs + (one_head ? 0 : j)].eG[ln];
                 arrive(G_FREE + gs);
+                wait(Y_FULL + j, 0);  // C h
+                __syncwarp();
+                tc::tc_after_sync();
+#pragma unroll
+                for (int n0 = 0; n0 < 64; n0 += 16) {
+                    float v[16];
+                    tc::tmem_ld16(ycol + n0, v);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2)
+                        t[(n0 + i) / 2] = __ffma2_rn(make_float2(eg, eg), make_float2(v[i], v[i + 1]), t[(n0 + i) / 2]);
+                }
+                tc::tc_before_sync();
+                arrive(Y_FREE + j);
+                wait(Y_FULL + j, 1);  // W x
+                __syncwarp();
+                tc::tc_after_sync();
+#pragma unroll
+                for (int n0 = 0; n0 < 64; n0 += 16) {
+                    float v[16];
+                    tc::tmem_ld16(ycol + n0, v);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2)
+                        t[(n0 + i) / 2] = __fadd2_rn(t[(n0 + i) / 2], make_float2(v[i], v[i + 1]));
+                }
+                tc::tc_before_sync();
+                arrive(Y_FREE + j);
+                // x is spent: its tile takes z, then y (each thread its own row)
+                wait(X_DONE + xb, xi / NXB);
+                if (a.z && hf.width) {
+                    if (first && !*abort_flag) {
+                        tc::mbar_arrive_expect_tx(&bars[Z_FULL + xb], K::TILE);
+                        tma_load_3d(base + K::OFF_X + xb * K::TILE, &p.z, hf.col, hf.head, row, &bars[Z_FULL + xb]);
+                        drain(&bars[Z_FULL + xb], (uint32_t)(xi / NXB) & 1u);
+                    }
+                    wait(Z_FULL + xb, xi / NXB);
+                }
+                const bool whole = c * L + L <= rows;
+                bf* y = static_cast<bf*>(a.y) + ((int64_t)(row + ln) * a.H + hf.head) * a.P + hf.col;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const uint32_t at = xrow + tc::sw128_off(ln, u);
+                    if (a.z) {
+                        const uint4 zu = tc::ld_shared_v4(at);
+                        const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            t[4 * u + i] = __fmul2_rn(t[4 * u + i], conv_silu2(make_float2(bf16_lo(zw[i]), bf16_hi(zw[i]))));
+                    }
+                    uint32_t ow[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) ow[i] = tc::pack_bf16(t[4 * u + i].x, t[4 * u + i].y);
+                    if (whole)
+                        tc::st_shared_v4(at, ow[0], ow[1], ow[2], ow[3]);
+                    else if (c * L + ln < rows && 8 * u < hf.width)  // rows behind belong to others
+                        *reinterpret_cast<uint4*>(y + 8 * u) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+                }
+                tc::fence_async_smem();
+                tc::named_bar(2 + j, 128);
+                if (first) {
+                    if (whole && hf.width && !*abort_flag) {
+                        tma_store_3d(&p.y, xrow, hf.col, hf.head, row);
+                        tc::bulk_commit();
+                        tc::bulk_wait_read0();
+                    }
+                    tc::mbar_arrive(&bars[X_FREE + xb]);
+                }
+                __syncwarp();
             }
+            if (first) tc::bulk_wait0();  // y is in global memory before the CTA leaves
         }
-    } else if (warp < 18) {
+    } else if (warp < 26) {
         // ============================================================ gate warps
-        const int j = warp - 16;
+        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        const int j = warp - 24;
         const Half hf = half_of(p, unit, j);
         const bool on = hf.width > 0 && !(one_head && j == 1);
         const float A2 = on ? -expf(a.A_log[hf.head]) * tcf::kLog2e : 0.f;
@@ -572,7 +646,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             Gates& G = gates[2 * gs + j];
             const int t = 4 * lane;
             *reinterpret_cast<float4*>(&G.pre[t]) = make_float4(p0, p1, p2, p3);
-            *reinterpret_cast<float4*>(&G.dt[t]) = make_float4(d[0], d[1], d[2], d[3]);
+            *reinterpret_cast<float4*>(&G.prd[t]) =
+                make_float4(log2f(d[0]) - p0, log2f(d[1]) - p1, log2f(d[2]) - p2, log2f(d[3]) - p3);
             *reinterpret_cast<float4*>(&G.col[t]) =
                 make_float4(d[0] * exp2f(s0), d[1] * exp2f(s1), d[2] * exp2f(s2), d[3] * exp2f(s3));
             *reinterpret_cast<float4*>(&G.w[t]) =
@@ -588,8 +663,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             }
             arrive(G_FULL + gs);
         }
-    } else if (warp == 18) {
+    } else if (warp == 26) {
         // ============================================================== TMA warp
+        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (lane == 0) {
             Half hf[2] = {half_of(p, unit, 0), half_of(p, unit, 1)};
             // a missing second head reads the first one's columns: nothing uses them
@@ -597,34 +673,33 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             int done = 0;
             for (int c = 0; c < nch && !*abort_flag; ++c) {
                 const int r = (int)(r0 + (int64_t)c * L), st = c & 1;
-                if (c >= 2 && !wait(B_FREE + st, (c >> 1) - 1)) break;
+                for (int j = 0; j < 2; ++j) {
+                    const int xi = 2 * c + j, xb = xi % NXB;
+                    if (xi >= NXB) wait((STATES ? X_DONE : X_FREE) + xb, xi / NXB - 1);
+                    tc::mbar_arrive_expect_tx(&bars[X_FULL + xb], K::TILE);
+                    tma_load_3d(base + K::OFF_X + xb * K::TILE, &p.x, hf[j].col, hf[j].head, r, &bars[X_FULL + xb]);
+                }
+                if (c >= 2) wait(B_FREE + st, (c >> 1) - 1);
                 tc::mbar_arrive_expect_tx(&bars[B_FULL + st], K::BT);
                 for (int h = 0; h < NH; ++h)
                     tma_load_3d(base + K::OFF_B + st * K::BT + h * K::TILE, &p.b, 64 * h, grp, r, &bars[B_FULL + st]);
                 if (!STATES) {
-                    if (c >= 2) wait(C_FREE_ + st, (c >> 1) - 1);
-                    tc::mbar_arrive_expect_tx(&bars[C_FULL_ + st], K::BT);
+                    if (c >= 1) wait(C_FREE_, c - 1);
+                    tc::mbar_arrive_expect_tx(&bars[C_FULL_], K::BT);
                     for (int h = 0; h < NH; ++h)
-                        tma_load_3d(base + K::OFF_C + st * K::BT + h * K::TILE, &p.c, 64 * h, grp, r, &bars[C_FULL_ + st]);
-                }
-                for (int j = 0; j < 2; ++j) {
-                    const int xi = 2 * c + j, xb = xi % NXB;
-                    if (xi >= NXB) wait(X_FREE + xb, xi / NXB - 1);
-                    tc::mbar_arrive_expect_tx(&bars[X_FULL + xb], K::TILE);
-                    tma_load_3d(base + K::OFF_X + xb * K::TILE, &p.x, hf[j].col, hf[j].head, r, &bars[X_FULL + xb]);
+                        tma_load_3d(base + K::OFF_C + h * K::TILE, &p.c, 64 * h, grp, r, &bars[C_FULL_]);
                 }
                 done = c + 1;
             }
             // never leave with a copy in flight
-            for (int c = done >= 2 ? done - 2 : 0; c < done; ++c) {
-                tcf::drain_wait(&bars[B_FULL + (c & 1)], (c >> 1) & 1);
-                if (!STATES) tcf::drain_wait(&bars[C_FULL_ + (c & 1)], (c >> 1) & 1);
-            }
+            for (int c = done >= 2 ? done - 2 : 0; c < done; ++c) drain(&bars[B_FULL + (c & 1)], (c >> 1) & 1);
+            if (!STATES && done > 0) drain(&bars[C_FULL_], (done - 1) & 1);
             for (int i = 2 * done >= NXB ? 2 * done - NXB : 0; i < 2 * done; ++i)
-                tcf::drain_wait(&bars[X_FULL + i % NXB], (i / NXB) & 1);
+                drain(&bars[X_FULL + i % NXB], (i / NXB) & 1);
         }
     } else {
         // ============================================================== MMA warp
+        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         constexpr uint32_t idCB = tc::idesc_bf16(128, 128, 0, 0), idY2 = tc::idesc_bf16(128, 64, 0, 0),
                            idY1 = tc::idesc_bf16(128, 64, 0, 1), idS = tc::idesc_bf16(128, NP, 0, 1);
         auto ready = [&](int b, int phase) {
@@ -653,18 +728,21 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             __syncwarp();
         };
         auto issue_y2 = [&](int c, int j) {
+            if (c > 0) ready(Y_FREE + j, 1);
             if (tc::elect_one()) {
-                const uint32_t lc = tc::desc_lo(sbase + K::OFF_C + (c & 1) * K::BT, 16),
+                const uint32_t lc = tc::desc_lo(sbase + K::OFF_C, 16),
                                lh = tc::desc_lo(sbase + K::OFF_H + j * 8192, 16);
-                tc::mma_ss<0>(tmem + K::COL_Y2, tc::desc(lc), tc::desc(lh), idY2);
+                const uint32_t d = tmem + K::COL_Y + 64 * j;
+                tc::mma_ss<0>(d, tc::desc(lc), tc::desc(lh), idY2);
 #pragma unroll
                 for (int k = 1; k < NP / 16; ++k) {
                     const uint32_t o = (k >> 2) * (K::TILE / 16) + (k & 3) * 2;
-                    tc::mma_ss<1>(tmem + K::COL_Y2, tc::desc(lc + o), tc::desc(lh + o), idY2);
+                    tc::mma_ss<1>(d, tc::desc(lc + o), tc::desc(lh + o), idY2);
                 }
+                tc::mma_commit(&bars[Y_FULL + j]);
                 if (j == 1) {
                     tc::mma_commit(&bars[H_FREE]);
-                    tc::mma_commit(&bars[C_FREE_ + (c & 1)]);
+                    tc::mma_commit(&bars[C_FREE_]);
                 }
             }
             __syncwarp();
@@ -672,57 +750,60 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         auto issue_y1 = [&](int c, int j) {
             const int xi = 2 * c + j, xb = xi % NXB;
             ready(X_FULL + xb, xi / NXB);
+            ready(Y_FREE + j, 0);
             if (tc::elect_one()) {
                 const uint32_t lx = tc::desc_lo(sbase + K::OFF_X + xb * K::TILE, K::TILE);
                 const uint32_t w = tmem + K::COL_CB + (one_head ? 0 : 16 * j);
-                tc::mma_ts<0>(tmem + K::COL_Y1, w, tc::desc(lx), idY1);
+                const uint32_t d = tmem + K::COL_Y + 64 * j;
+                tc::mma_ts<0>(d, w, tc::desc(lx), idY1);
 #pragma unroll
                 for (int k = 1; k < 8; ++k)
-                    tc::mma_ts<1>(tmem + K::COL_Y1, w + 32 * (k >> 1) + 8 * (k & 1), tc::desc(lx + 128 * k), idY1);
-                tc::mma_commit(&bars[Y_FULL]);
-                tc::mma_commit(&bars[X_FREE + xb]);
+                    tc::mma_ts<1>(d, w + 32 * (k >> 1) + 8 * (k & 1), tc::desc(lx + 128 * k), idY1);
+                tc::mma_commit(&bars[Y_FULL + j]);
+                tc::mma_commit(&bars[X_DONE + xb]);
                 if (j == 1) tc::mma_commit(&bars[W_FREE]);
             }
             __syncwarp();
         };
-        for (int c = 0; c < nch; ++c) {
+        auto issue_cb = [&](int c) {
             ready(B_FULL + (c & 1), c >> 1);
             if (c == nch - 1 && tail < L) ready(CLEAN, 0);
+            ready(C_FULL_, c);
+            if (c > 0) ready(W_FREE, c - 1);  // the last chunk's W has been read
+            if (tc::elect_one()) {
+                const uint32_t lc = tc::desc_lo(sbase + K::OFF_C, 16),
+                               lb = tc::desc_lo(sbase + K::OFF_B + (c & 1) * K::BT, 16);
+                tc::mma_ss<0>(tmem + K::COL_CB, tc::desc(lc), tc::desc(lb), idCB);
+#pragma unroll
+                for (int k = 1; k < NP / 16; ++k) {
+                    const uint32_t o = (k >> 2) * (K::TILE / 16) + (k & 3) * 2;
+                    tc::mma_ss<1>(tmem + K::COL_CB, tc::desc(lc + o), tc::desc(lb + o), idCB);
+                }
+                tc::mma_commit(&bars[CB_FULL]);
+            }
+            __syncwarp();
+        };
+        // Per chunk: C B^T, then C h and the state's products, under which the M warps make
+        // W; then W x, under which the S warps hand over the next chunk's state.
+        for (int c = 0; c < nch; ++c) {
             if constexpr (STATES) {
+                ready(B_FULL + (c & 1), c >> 1);
                 ready(S_READY, c);
                 for (int k = 0; k < 4; ++k) issue_s(c, k);
             } else {
-                ready(C_FULL_ + (c & 1), c >> 1);
-                if (c > 0) ready(W_FREE, c - 1);  // the last chunk's W has been read
-                if (tc::elect_one()) {
-                    const uint32_t lc = tc::desc_lo(sbase + K::OFF_C + (c & 1) * K::BT, 16),
-                                   lb = tc::desc_lo(sbase + K::OFF_B + (c & 1) * K::BT, 16);
-                    tc::mma_ss<0>(tmem + K::COL_CB, tc::desc(lc), tc::desc(lb), idCB);
-#pragma unroll
-                    for (int k = 1; k < NP / 16; ++k) {
-                        const uint32_t o = (k >> 2) * (K::TILE / 16) + (k & 3) * 2;
-                        tc::mma_ss<1>(tmem + K::COL_CB, tc::desc(lc + o), tc::desc(lb + o), idCB);
-                    }
-                    tc::mma_commit(&bars[CB_FULL]);
-                }
-                __syncwarp();
+                issue_cb(c);
                 ready(S_READY, c);
-                if (c > 0) ready(Y_FREE, 2 * c - 1);
                 issue_y2(c, 0);
-                issue_s(c, 0);
-                issue_s(c, 1);
+                issue_y2(c, 1);
+                for (int k = 0; k < 4; ++k) issue_s(c, k);
                 ready(M_FULL, c);
                 issue_y1(c, 0);
-                issue_s(c, 2);
-                issue_s(c, 3);
-                ready(Y_FREE, 2 * c);
-                issue_y2(c, 1);
                 issue_y1(c, 1);
             }
         }
         if (tc::elect_one()) {  // never leave with a product in flight
             tc::mma_commit(&bars[S_DRAIN]);
-            tcf::drain_wait(&bars[S_DRAIN], 0);
+            drain(&bars[S_DRAIN], 0);
         }
         __syncwarp();
     }
@@ -863,7 +944,8 @@ inline cudaError_t launch_scan_tc(const ScanArgs& a, int64_t rows, const ScanPla
     ScanTcArgs p;
     memset(&p, 0, sizeof(p));
     if (!make_map3(&p.x, a.x, a.P, a.H, rows, a.xs) || !make_map3(&p.b, a.Bm, a.N, a.G, rows, a.bs) ||
-        !make_map3(&p.c, a.Cm, a.N, a.G, rows, a.cs))
+        !make_map3(&p.c, a.Cm, a.N, a.G, rows, a.cs) || (a.z && !make_map3(&p.z, a.z, a.P, a.H, rows, a.zs)) ||
+        !make_map3(&p.y, a.y, a.P, a.H, rows, (int64_t)a.H * a.P))
         return cudaErrorInvalidValue;
     p.a = a;
     p.pairs = r.pairs;
