@@ -23,7 +23,7 @@
 // A CTA owns 128 value lanes (two heads of 64 or 32 value columns of one group, or
 // one head of 128) of one segment of a sequence.  Twenty warps, each with one job:
 //   X (4)  reads x, writes the split (w x)^T to tensor memory, 32 tokens at a time
-//   M (4)  turns CB into W          S (4)  decays S, hands its bf16 copy to C h
+//   M (8)  turns CB into W          S (4)  decays S, hands its bf16 copy to C h
 //   Y (4)  y = Y1 + e^G Y2 + D x, gate, store      gates (2), TMA (1), MMA (1)
 // The tensor pipe is the bound (N = 128: 3300 cycles of products a chunk); the MMA
 // warp orders the products so that each wait falls under another product.
@@ -129,6 +129,21 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, i
                  "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
+// Four 8 x 8 matrices of 16-bit elements, transposed: thread t of the warp gets rows
+// 2 (t % 4), + 1 (low, high half) of column t / 4.  Row addresses of matrix i from lanes 8 i ...
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// 16 lanes x 16 columns of tensor memory: r[2 i] is lane t / 4, r[2 i + 1] lane 8 + t / 4, both
+// column 4 i + t % 4.
+__device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
@@ -225,10 +240,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     if (threadIdx.x == 0) {
         for (int i = 0; i < N_SCAN_BARS; ++i) {
             uint32_t n = 1;
-            if (i >= X_DONE && i < X_DONE + NXB) n = STATES ? 4 : 9;  // X warps (, Y warps, the product)
+            if (i >= X_DONE && i < X_DONE + NXB) n = STATES ? 4 : 7;  // X warps (, Y warps, the product)
             if (i >= G_FULL && i < G_FULL + NGR) n = 2;
             if (i >= G_FREE && i < G_FREE + NGR) n = STATES ? 12 : 24;
-            if (i == M_FULL || i == XQ_FULL || i == XQ_FULL + 1 || i == S_READY || i == Y_FREE ||
+            if (i == M_FULL) n = 8;
+            if (i == XQ_FULL || i == XQ_FULL + 1 || i == S_READY || i == Y_FREE ||
                 i == Y_FREE + 1 || i == CLEAN)
                 n = 4;
             mbar_init(&bars[i], n);
@@ -250,76 +266,76 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     const int q = warp & 3, ln = 32 * q + lane;  // tensor-memory lane of the four-warp jobs
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
 
-    if (warp < 8) {
+    if (warp < (STATES ? 8 : 4)) {
         // =============================================================== X warps
-        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        // warpgroup k & 1 takes the quarters k and k + 2 of a chunk, through its own
-        // buffer of tensor memory
-        const int set = warp >> 2;
-        const int j = ln >> 6, pc = ln & 63;   // half, value column within it
-        uint32_t off[8];
+        // A chunk goes through in quarters of 32 tokens and two buffers of tensor memory
+        // (the first pass has two warpgroups for it, a buffer each).  x^T comes out of
+        // shared memory by transposing 8 x 8 loads: a thread gets two tokens of a value
+        // column, the layout in which 16 lanes x 4 columns go to tensor memory.
+        constexpr int SETS = STATES ? 2 : 1;
+        const int j = q >> 1;                  // half
+        const int tr = lane & 7, tm = lane >> 3;
+        uint32_t off[2];                       // of the loads of value columns 16 hb .. + 16
 #pragma unroll
-        for (int t = 0; t < 8; ++t) off[t] = t * 128 + ((((uint32_t)pc >> 3) ^ t) << 4) + (pc & 7) * 2;
-        const uint32_t col = lane_base + K::COL_WX + 48 * set;
+        for (int hb = 0; hb < 2; ++hb)
+            off[hb] = (tm >> 1) * 1024 + tr * 128 + (((uint32_t)(4 * (q & 1) + 2 * hb + (tm & 1)) ^ tr) << 4);
         for (int c = 0; c < nch; ++c) {
             const int gs = c % NGR, xi = 2 * c + j, xb = xi % NXB;
             if (c == nch - 1 && tail < L) {
                 // rows behind the sequence's end belong to another one: x and B to zero
                 // (a zero weight would still carry a NaN through the products)
-                if (set == 0) {
-                    for (int h = 0; h < 2; ++h) wait(X_FULL + (2 * c + h) % NXB, (2 * c + h) / NXB);
-                    wait(B_FULL + (c & 1), c >> 1);
-                    if (ln >= tail) {
-                        const uint32_t row = (uint32_t)ln * 128u;
-                        for (int i = 0; i < 8; ++i) {
-                            for (int h = 0; h < 2; ++h)
-                                tc::st_shared_v4(sbase + K::OFF_X + ((2 * c + h) % NXB) * K::TILE + row + 16 * i, 0, 0, 0, 0);
-                            for (int h = 0; h < NH; ++h)
-                                tc::st_shared_v4(sbase + K::OFF_B + (c & 1) * K::BT + h * K::TILE + row + 16 * i, 0, 0, 0, 0);
-                        }
+                for (int h = 0; h < 2; ++h) wait(X_FULL + (2 * c + h) % NXB, (2 * c + h) / NXB);
+                wait(B_FULL + (c & 1), c >> 1);
+                if (ln >= tail) {
+                    const uint32_t row = (uint32_t)ln * 128u;
+                    for (int i = 0; i < 8; ++i) {
+                        for (int h = 0; h < 2; ++h)
+                            tc::st_shared_v4(sbase + K::OFF_X + ((2 * c + h) % NXB) * K::TILE + row + 16 * i, 0, 0, 0, 0);
+                        for (int h = 0; h < NH; ++h)
+                            tc::st_shared_v4(sbase + K::OFF_B + (c & 1) * K::BT + h * K::TILE + row + 16 * i, 0, 0, 0, 0);
                     }
-                    tc::fence_async_smem();
                 }
-                tc::named_bar(1, 256);
-                if (set == 0) arrive(CLEAN);
+                tc::fence_async_smem();
+                tc::named_bar(1, 128);  // (a segment that is not a sequence's last has no tail)
+                arrive(CLEAN);
             }
             wait(X_FULL + xb, xi / NXB);
             wait(G_FULL + gs, c / NGR);
-            const float* w = gates[2 * gs + (one_head ? 0 : j)].w + 32 * set;
-            const uint8_t* xt = base + K::OFF_X + xb * K::TILE + 4096 * set;
+            const float* w = gates[2 * gs + (one_head ? 0 : j)].w + 2 * (lane & 3);
+            const uint32_t xt = sbase + K::OFF_X + xb * K::TILE;
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {  // 16 tokens: 32 set + 64 (k / 2) + 16 (k % 2)
-                const int t0 = 64 * (k >> 1) + 16 * (k & 1);
-                const uint8_t* rows8 = xt + t0 * 128;
-                uint32_t hi[8], mi[8], lo[8];
+            for (int k = warp >> 2; k < 4; k += SETS) {
+                const int buf = k & 1, use = 2 * c + (k >> 1);
+                const uint32_t col = lane_base + K::COL_WX + 48 * buf;
+                float2 wv[4];
 #pragma unroll
-                for (int t = 0; t < 16; t += 2) {
-                    const float2 wv = *reinterpret_cast<const float2*>(&w[t0 + t]);
-                    const uint8_t* row = rows8 + (t >> 3) * 1024;
-                    const uint32_t x0 = *reinterpret_cast<const uint16_t*>(row + off[t & 7]),
-                                   x1 = *reinterpret_cast<const uint16_t*>(row + off[(t + 1) & 7]);
-                    // 24 bits in three truncated terms of 8: the last is exact
-                    const float2 v = __fmul2_rn(make_float2(bf16_lo(x0), bf16_lo(x1)), wv);
-                    const float2 m = __fadd2_rn(v, make_float2(-bf16_hi(__float_as_uint(v.x)), -bf16_hi(__float_as_uint(v.y))));
-                    const float2 l = __fadd2_rn(m, make_float2(-bf16_hi(__float_as_uint(m.x)), -bf16_hi(__float_as_uint(m.y))));
-                    hi[t / 2] = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
-                    mi[t / 2] = __byte_perm(__float_as_uint(m.x), __float_as_uint(m.y), 0x7632);
-                    lo[t / 2] = __byte_perm(__float_as_uint(l.x), __float_as_uint(l.y), 0x7632);
+                for (int i = 0; i < 4; ++i) wv[i] = *reinterpret_cast<const float2*>(&w[32 * k + 8 * i]);
+                if (use > 0) wait(XQ_FREE + buf, use - 1);
+                __syncwarp();
+                tc::tc_after_sync();
+#pragma unroll 1
+                for (int hb = 0; hb < 2; ++hb) {
+                    uint32_t x[8], hi[8], mi[8], lo[8];
+                    ldmatrix4_trans(xt + 4096 * k + (hb ? off[1] : off[0]), x);
+                    ldmatrix4_trans(xt + 4096 * k + 2048 + (hb ? off[1] : off[0]), x + 4);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        // 24 bits in three truncated terms of 8: the last is exact
+                        const float2 v = __fmul2_rn(make_float2(bf16_lo(x[i]), bf16_hi(x[i])), wv[i >> 1]);
+                        const float2 m = __fadd2_rn(v, make_float2(-bf16_hi(__float_as_uint(v.x)), -bf16_hi(__float_as_uint(v.y))));
+                        const float2 l = __fadd2_rn(m, make_float2(-bf16_hi(__float_as_uint(m.x)), -bf16_hi(__float_as_uint(m.y))));
+                        hi[i] = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
+                        mi[i] = __byte_perm(__float_as_uint(m.x), __float_as_uint(m.y), 0x7632);
+                        lo[i] = __byte_perm(__float_as_uint(l.x), __float_as_uint(l.y), 0x7632);
+                    }
+                    const uint32_t at = col + ((uint32_t)(16 * hb) << 16);
+                    tmem_st_16x128(at, hi);
+                    tmem_st_16x128(at + 16, mi);
+                    tmem_st_16x128(at + 32, lo);
                 }
-                const int use = 2 * c + (k >> 1);  // of this buffer
-                if ((k & 1) == 0) {
-                    if (use > 0) wait(XQ_FREE + set, use - 1);
-                    __syncwarp();
-                    tc::tc_after_sync();
-                }
-                tc::tmem_st8(col + 8 * (k & 1), hi);
-                tc::tmem_st8(col + 16 + 8 * (k & 1), mi);
-                tc::tmem_st8(col + 32 + 8 * (k & 1), lo);
-                if (k & 1) {
-                    tc::tmem_wait_st();
-                    tc::tc_before_sync();
-                    arrive(XQ_FULL + set);
-                }
+                tc::tmem_wait_st();
+                tc::tc_before_sync();
+                arrive(XQ_FULL + buf);
             }
             arrive(X_DONE + xb);
             arrive(G_FREE + gs);
@@ -330,6 +346,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         if constexpr (!STATES) {
             const uint32_t zero[16] = {};
             const int heads = one_head ? 1 : 2;
+            const int jb0 = 2 * ((warp >> 2) - 1);  // blocks of 32 columns jb0, jb0 + 1
             for (int c = 0; c < nch; ++c) {
                 const int gs = c % NGR;
                 wait(G_FULL + gs, c / NGR);
@@ -337,7 +354,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 __syncwarp();
                 tc::tc_after_sync();
 #pragma unroll 1
-                for (int jb = 0; jb < 4; ++jb) {
+                for (int jb = jb0; jb < jb0 + 2; ++jb) {
                     const uint32_t col = lane_base + K::COL_CB + 32 * jb;
                     if (jb > q) {  // above the diagonal
                         tc::tmem_st16(col, zero);
@@ -359,11 +376,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                             for (int s0 = 0; s0 < 32; s0 += 16) {
                                 uint32_t o[8];
 #pragma unroll
-                                for (int s = 0; s < 16; s += 2) {
-                                    const float2 f = *reinterpret_cast<const float2*>(&G.col[32 * jb + s0 + s]);
+                                for (int s = 0; s < 16; s += 4) {
+                                    const float4 f = *reinterpret_cast<const float4*>(&G.col[32 * jb + s0 + s]);
                                     const float2 m = __fmul2_rn(make_float2(v[s0 + s], v[s0 + s + 1]),
-                                                                __fmul2_rn(make_float2(rf, rf), f));
+                                                                __fmul2_rn(make_float2(rf, rf), make_float2(f.x, f.y)));
+                                    const float2 n = __fmul2_rn(make_float2(v[s0 + s + 2], v[s0 + s + 3]),
+                                                                __fmul2_rn(make_float2(rf, rf), make_float2(f.z, f.w)));
                                     o[s / 2] = tc::pack_bf16(m.x, m.y);
+                                    o[s / 2 + 1] = tc::pack_bf16(n.x, n.y);
                                 }
                                 tc::tmem_st8(col + 16 * h + s0 / 2, o);
                             }
@@ -481,7 +501,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         }
     } else if (warp < 24) {
         // =============================================================== Y warps
-        if constexpr (!STATES) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        if constexpr (!STATES) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
         // warpgroup j: half j, one token a thread
         if constexpr (!STATES) {
             using bf = __nv_bfloat16;
@@ -588,7 +608,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         }
     } else if (warp < 26) {
         // ============================================================ gate warps
-        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int j = warp - 24;
         const Half hf = half_of(p, unit, j);
         const bool on = hf.width > 0 && !(one_head && j == 1);
@@ -665,7 +685,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         }
     } else if (warp == 26) {
         // ============================================================== TMA warp
-        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (lane == 0) {
             Half hf[2] = {half_of(p, unit, 0), half_of(p, unit, 1)};
             // a missing second head reads the first one's columns: nothing uses them
@@ -699,8 +719,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         }
     } else {
         // ============================================================== MMA warp
-        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        constexpr uint32_t idCB = tc::idesc_bf16(128, 128, 0, 0), idY2 = tc::idesc_bf16(128, 64, 0, 0),
+        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        constexpr uint32_t idCB = tc::idesc_bf16(128, 128, 0, 0),
                            idY1 = tc::idesc_bf16(128, 64, 0, 1), idS = tc::idesc_bf16(128, NP, 0, 1);
         auto ready = [&](int b, int phase) {
             tcf::wait_warp(&bars[b], (uint32_t)phase & 1u, abort_flag);
@@ -727,23 +747,23 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             }
             __syncwarp();
         };
-        auto issue_y2 = [&](int c, int j) {
-            if (c > 0) ready(Y_FREE + j, 1);
+        auto issue_y2 = [&](int c) {
+            if (c > 0) {
+                ready(Y_FREE, 1);
+                ready(Y_FREE + 1, 1);
+            }
             if (tc::elect_one()) {
-                const uint32_t lc = tc::desc_lo(sbase + K::OFF_C, 16),
-                               lh = tc::desc_lo(sbase + K::OFF_H + j * 8192, 16);
-                const uint32_t d = tmem + K::COL_Y + 64 * j;
-                tc::mma_ss<0>(d, tc::desc(lc), tc::desc(lh), idY2);
+                const uint32_t lc = tc::desc_lo(sbase + K::OFF_C, 16), lh = tc::desc_lo(sbase + K::OFF_H, 16);
+                tc::mma_ss<0>(tmem + K::COL_Y, tc::desc(lc), tc::desc(lh), idCB);
 #pragma unroll
                 for (int k = 1; k < NP / 16; ++k) {
                     const uint32_t o = (k >> 2) * (K::TILE / 16) + (k & 3) * 2;
-                    tc::mma_ss<1>(d, tc::desc(lc + o), tc::desc(lh + o), idY2);
+                    tc::mma_ss<1>(tmem + K::COL_Y, tc::desc(lc + o), tc::desc(lh + o), idCB);
                 }
-                tc::mma_commit(&bars[Y_FULL + j]);
-                if (j == 1) {
-                    tc::mma_commit(&bars[H_FREE]);
-                    tc::mma_commit(&bars[C_FREE_]);
-                }
+                tc::mma_commit(&bars[Y_FULL]);
+                tc::mma_commit(&bars[Y_FULL + 1]);
+                tc::mma_commit(&bars[H_FREE]);
+                tc::mma_commit(&bars[C_FREE_]);
             }
             __syncwarp();
         };
@@ -793,8 +813,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             } else {
                 issue_cb(c);
                 ready(S_READY, c);
-                issue_y2(c, 0);
-                issue_y2(c, 1);
+                issue_y2(c);
                 for (int k = 0; k < 4; ++k) issue_s(c, k);
                 ready(M_FULL, c);
                 issue_y1(c, 0);
