@@ -42,14 +42,13 @@ namespace ssm {
 constexpr int L = 128;          // tokens of a chunk
 constexpr int kScanThreads = 896;
 constexpr int NGR = 3;          // gate ring
-constexpr int NXB = 5;           // half-tiles of x in flight (then of z, then of y)
+constexpr int NXB = 3;          // half-tiles of x in flight
 constexpr float kMinG2 = -160.f;  // 2^-160 is 0 in fp32: more decay changes nothing
 
 struct Gates {                  // of one chunk and head; sums in log2 units
     float pre[L];               // inclusive sum within the token's block of 32
     float col[L];               // dt 2^(sum behind the token within its block)
     float w[L];                 // dt 2^(sum behind the token within the chunk)
-    float eG[L];                // 2^(inclusive sum within the chunk)
     float prd[L];               // log2(dt) - pre
     float tot[4];               // block sums
     float last;                 // 2^(sum of the chunk)
@@ -75,7 +74,8 @@ struct ScanCfg {
     static constexpr uint32_t OFF_B = 0;                // [2]
     static constexpr uint32_t OFF_C = OFF_B + 2 * BT;
     static constexpr uint32_t OFF_X = OFF_C + BT;       // [NXB]
-    static constexpr uint32_t OFF_H = OFF_X + NXB * TILE;
+    static constexpr uint32_t OFF_Z = OFF_X + NXB * TILE;  // [2 halves] z, then y in its place
+    static constexpr uint32_t OFF_H = OFF_Z + 2 * TILE;
     static constexpr uint32_t OFF_G = OFF_H + BT;       // [NGR][2] Gates
     static constexpr uint32_t OFF_BAR = OFF_G + NGR * 2 * (uint32_t)sizeof(Gates);
     static constexpr uint32_t SMEM = OFF_BAR + 52 * 8 + 16 + 1024;
@@ -83,16 +83,16 @@ struct ScanCfg {
     // tensor memory columns
     static constexpr uint32_t COL_CB = 0;               // fp32 CB, then W of both heads
     static constexpr uint32_t COL_S = 128;              // S, lane = value lane, NP columns
-    static constexpr uint32_t COL_Y = COL_S + NP;       // [2 halves] x 64: Y1, then Y2
+    static constexpr uint32_t COL_Y = COL_S + NP;       // [2 halves] x 64
     static constexpr uint32_t COL_WX = COL_Y + 128;     // [2] x 48: three terms of 32 tokens
     static_assert(COL_WX + 96 <= 512, "tensor memory budget");
 };
 
 enum : int {
     B_FULL = 0, B_FREE = B_FULL + 2, C_FULL_ = B_FREE + 2, C_FREE_, X_FULL, X_DONE = X_FULL + NXB,
-    Z_FULL = X_DONE + NXB, X_FREE = Z_FULL + NXB, G_FULL = X_FREE + NXB, G_FREE = G_FULL + NGR,
-    CB_FULL = G_FREE + NGR, M_FULL, W_FREE, XQ_FULL, XQ_FREE = XQ_FULL + 2, S_READY = XQ_FREE + 2, DS_DONE,
-    H_FREE, Y_FULL, Y_FREE = Y_FULL + 2, CLEAN = Y_FREE + 2, S_DRAIN, N_SCAN_BARS
+    Z_FULL = X_DONE + NXB, G_FULL = Z_FULL + 2, G_FREE = G_FULL + NGR, CB_FULL = G_FREE + NGR, M_FULL, W_FREE,
+    XQ_FULL, XQ_FREE = XQ_FULL + 2, S_READY = XQ_FREE + 2, DS_DONE, H_FREE, Y_FULL, Y_FREE = Y_FULL + 2,
+    CLEAN = Y_FREE + 2, S_DRAIN, N_SCAN_BARS
 };
 static_assert(N_SCAN_BARS <= 52, "barrier slots");
 
@@ -121,12 +121,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
                  "r"(x), "r"(y), "r"(z), "r"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
 // Four 8 x 8 matrices of 16-bit elements, transposed: thread t of the warp gets rows
@@ -207,8 +201,8 @@ __device__ __forceinline__ Half half_of(const ScanTcArgs& p, int unit, int j) {
     return Half{g * per + h, 0, h < per ? p.a.P : 0};
 }
 
-// Grid: segments * units.
-template <int NP, bool STATES>
+// Grid: segments * units.  ONE: the 128 lanes are one head (P = 128).
+template <int NP, bool STATES, bool ONE>
 __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_constant__ ScanTcArgs p) {
     using K = ScanCfg<NP>;
     constexpr int NH = K::NH;
@@ -235,12 +229,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     const int nch = (int)__reduce_max_sync(0xffffffffu, (uint32_t)((rows + L - 1) / L));
     const int tail = rows - (nch - 1) * L;  // rows of the last chunk
     const int grp = unit / p.pairs;
-    const bool one_head = a.P == 128;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < N_SCAN_BARS; ++i) {
             uint32_t n = 1;
-            if (i >= X_DONE && i < X_DONE + NXB) n = STATES ? 4 : 7;  // X warps (, Y warps, the product)
+            if (i >= X_DONE && i < X_DONE + NXB) n = STATES ? 4 : 3;  // X warps (, the product)
             if (i >= G_FULL && i < G_FULL + NGR) n = 2;
             if (i >= G_FREE && i < G_FREE + NGR) n = STATES ? 12 : 24;
             if (i == M_FULL) n = 8;
@@ -301,7 +294,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             }
             wait(X_FULL + xb, xi / NXB);
             wait(G_FULL + gs, c / NGR);
-            const float* w = gates[2 * gs + (one_head ? 0 : j)].w + 2 * (lane & 3);
+            const float* w = gates[2 * gs + (ONE ? 0 : j)].w + 2 * (lane & 3);
             const uint32_t xt = sbase + K::OFF_X + xb * K::TILE;
 #pragma unroll 1
             for (int k = warp >> 2; k < 4; k += SETS) {
@@ -342,69 +335,86 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         }
     } else if (warp < 12) {
         // =============================================================== M warps
-        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if constexpr (!STATES) {
             const uint32_t zero[16] = {};
-            const int heads = one_head ? 1 : 2;
-            const int jb0 = 2 * ((warp >> 2) - 1);  // blocks of 32 columns jb0, jb0 + 1
+            constexpr int HEADS = ONE ? 1 : 2;
+            const int kb0 = (warp >> 2) - 1;  // this warpgroup's blocks of 16 tokens: kb0, kb0 + 2, ...
+            float Dh[HEADS];
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h) {
+                const Half hf = half_of(p, unit, h);
+                Dh[h] = a.D && hf.width ? a.D[hf.head] : 0.f;
+            }
             for (int c = 0; c < nch; ++c) {
                 const int gs = c % NGR;
+                const Gates* G = &gates[2 * gs];
                 wait(G_FULL + gs, c / NGR);
+                // row factors of the earlier blocks of 32, while CB is under way
+                float pr[HEADS], rf[HEADS][3];
+#pragma unroll
+                for (int h = 0; h < HEADS; ++h) {
+                    pr[h] = G[h].pre[ln];
+                    float e = pr[h];
+#pragma unroll
+                    for (int b = 2; b >= 0; --b)
+                        if (b < q) {
+                            rf[h][b] = ex2_approx(e);
+                            e += G[h].tot[b];
+                        }
+                }
                 wait(CB_FULL, c);
                 __syncwarp();
                 tc::tc_after_sync();
-#pragma unroll 1
-                for (int jb = jb0; jb < jb0 + 2; ++jb) {
-                    const uint32_t col = lane_base + K::COL_CB + 32 * jb;
-                    if (jb > q) {  // above the diagonal
-                        tc::tmem_st16(col, zero);
-                        tc::tmem_st16(col + 16, zero);
-                        continue;
+                // 16 columns of CB become 8 of each head's W
+#pragma unroll
+                for (int b = 0; b < 3; ++b)
+                    if (b < q) {
+                        const int kb = 2 * b + kb0;
+                        const uint32_t col = lane_base + K::COL_CB + 16 * kb;
+                        float v[16];
+                        tc::tmem_ld16(col, v);
+                        tc::tmem_wait_ld();
+                        uint32_t o[HEADS][8];
+#pragma unroll
+                        for (int s = 0; s < 16; s += 4)
+#pragma unroll
+                            for (int h = 0; h < HEADS; ++h) {
+                                const float4 f = *reinterpret_cast<const float4*>(&G[h].col[16 * kb + s]);
+                                const float2 r2 = make_float2(rf[h][b], rf[h][b]);
+                                const float2 m = __fmul2_rn(make_float2(v[s], v[s + 1]), __fmul2_rn(r2, make_float2(f.x, f.y)));
+                                const float2 n = __fmul2_rn(make_float2(v[s + 2], v[s + 3]), __fmul2_rn(r2, make_float2(f.z, f.w)));
+                                o[h][s / 2] = tc::pack_bf16(m.x, m.y);
+                                o[h][s / 2 + 1] = tc::pack_bf16(n.x, n.y);
+                            }
+#pragma unroll
+                        for (int h = 0; h < HEADS; ++h) tc::tmem_st8(col + 8 * h, o[h]);
                     }
-                    float v[32];
-                    tc::tmem_ld32(col, v);
+                {  // the block on the diagonal, which is at s == r
+                    const int kb = 2 * q + kb0, r = ln - 16 * kb;
+                    const uint32_t col = lane_base + K::COL_CB + 16 * kb;
+                    float v[16];
+                    tc::tmem_ld16(col, v);
                     tc::tmem_wait_ld();
-#pragma unroll 1
-                    for (int h = 0; h < heads; ++h) {
-                        const Gates& G = gates[2 * gs + h];
-                        const float pr = G.pre[ln];
-                        if (jb < q) {
-                            float e = pr;
-                            for (int b = jb + 1; b < q; ++b) e += G.tot[b];
-                            const float rf = ex2_approx(e);
+                    uint32_t o[HEADS][8];
 #pragma unroll
-                            for (int s0 = 0; s0 < 32; s0 += 16) {
-                                uint32_t o[8];
+                    for (int s = 0; s < 16; s += 4)
 #pragma unroll
-                                for (int s = 0; s < 16; s += 4) {
-                                    const float4 f = *reinterpret_cast<const float4*>(&G.col[32 * jb + s0 + s]);
-                                    const float2 m = __fmul2_rn(make_float2(v[s0 + s], v[s0 + s + 1]),
-                                                                __fmul2_rn(make_float2(rf, rf), make_float2(f.x, f.y)));
-                                    const float2 n = __fmul2_rn(make_float2(v[s0 + s + 2], v[s0 + s + 3]),
-                                                                __fmul2_rn(make_float2(rf, rf), make_float2(f.z, f.w)));
-                                    o[s / 2] = tc::pack_bf16(m.x, m.y);
-                                    o[s / 2 + 1] = tc::pack_bf16(n.x, n.y);
-                                }
-                                tc::tmem_st8(col + 16 * h + s0 / 2, o);
-                            }
-                        } else {
+                        for (int h = 0; h < HEADS; ++h) {
+                            // 2^(pre_r - pre_s) dt_s with dt in the exponent
+                            const float4 f = *reinterpret_cast<const float4*>(&G[h].prd[16 * kb + s]);
+                            float m[4] = {v[s] * ex2_approx(pr[h] + f.x), v[s + 1] * ex2_approx(pr[h] + f.y),
+                                          v[s + 2] * ex2_approx(pr[h] + f.z), v[s + 3] * ex2_approx(pr[h] + f.w)};
 #pragma unroll
-                            for (int s0 = 0; s0 < 32; s0 += 16) {
-                                uint32_t o[8];
-#pragma unroll
-                                for (int s = 0; s < 16; s += 2) {
-                                    // 2^(pre_r - pre_s) dt_s with dt in the exponent
-                                    const float2 f = *reinterpret_cast<const float2*>(&G.prd[32 * jb + s0 + s]);
-                                    const float2 d = __fadd2_rn(make_float2(pr, pr), f);
-                                    const float2 m = __fmul2_rn(make_float2(v[s0 + s], v[s0 + s + 1]),
-                                                                make_float2(ex2_approx(d.x), ex2_approx(d.y)));
-                                    o[s / 2] = tc::pack_bf16(s0 + s <= lane ? m.x : 0.f, s0 + s + 1 <= lane ? m.y : 0.f);
-                                }
-                                tc::tmem_st8(col + 16 * h + s0 / 2, o);
-                            }
+                            for (int i = 0; i < 4; ++i)  // the skip D x rides on the diagonal
+                                m[i] = s + i < r ? m[i] : (s + i == r ? m[i] + Dh[h] : 0.f);
+                            o[h][s / 2] = tc::pack_bf16(m[0], m[1]);
+                            o[h][s / 2 + 1] = tc::pack_bf16(m[2], m[3]);
                         }
-                    }
+#pragma unroll
+                    for (int h = 0; h < HEADS; ++h) tc::tmem_st8(col + 8 * h, o[h]);
                 }
+                for (int b = q + 1; b < 4; ++b)  // above it
+                    tc::tmem_st16(lane_base + K::COL_CB + 16 * (2 * b + kb0), zero);
                 tc::tmem_wait_st();
                 tc::tc_before_sync();
                 arrive(M_FULL);
@@ -413,7 +423,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         }
     } else if (warp < 16) {
         // =============================================================== S warps
-        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int j = ln >> 6, pc = ln & 63;
         const Half hf = half_of(p, unit, j);
         const bool live = pc < hf.width;
@@ -443,7 +452,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         for (int c = 0; c < nch; ++c) {
             const int gs = c % NGR;
             wait(G_FULL + gs, c / NGR);
-            const Gates& G = gates[2 * gs + (one_head ? 0 : j)];
+            const Gates& G = gates[2 * gs + (ONE ? 0 : j)];
             const float e = G.last;
             sum_g += G.lastg;
             if (c > 0) wait(DS_DONE, c - 1);
@@ -501,125 +510,120 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         }
     } else if (warp < 24) {
         // =============================================================== Y warps
-        if constexpr (!STATES) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
         // warpgroup j: half j, one token a thread
         if constexpr (!STATES) {
             using bf = __nv_bfloat16;
             const int j = (warp >> 2) & 1;
             const Half hf = half_of(p, unit, j);
-            const float2 Dh = make_float2(a.D && hf.width ? a.D[hf.head] : 0.f, a.D && hf.width ? a.D[hf.head] : 0.f);
             const uint32_t ycol = lane_base + K::COL_Y + 64 * j;
+            const uint32_t tile = sbase + K::OFF_Z + j * K::TILE;
             const bool first = (warp & 3) == 0 && lane == 0;
+            // z of chunk c, once the last y has left the tile
+            auto next_z = [&](int c) {
+                tc::bulk_wait_read0();
+                if (a.z && hf.width && !*abort_flag) {
+                    tc::mbar_arrive_expect_tx(&bars[Z_FULL + j], K::TILE);
+                    tma_load_3d(base + K::OFF_Z + j * K::TILE, &p.z, hf.col, hf.head, (int)r0 + c * L, &bars[Z_FULL + j]);
+                } else {
+                    tc::mbar_arrive(&bars[Z_FULL + j]);
+                }
+            };
             for (int c = 0; c < nch; ++c) {
-                const int gs = c % NGR, xi = 2 * c + j, xb = xi % NXB;
+                const int gs = c % NGR;
                 const int row = (int)r0 + c * L;
-                float2 t[32];
-                wait(X_FULL + xb, xi / NXB);
-                if (first && a.z && hf.width) tma_prefetch_3d(&p.z, hf.col, hf.head, row);
-                const uint32_t xrow = sbase + K::OFF_X + xb * K::TILE;
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    if (a.D) {
-                        const uint4 xv = tc::ld_shared_v4(xrow + tc::sw128_off(ln, u));
-                        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            t[4 * u + i] = __fmul2_rn(Dh, make_float2(bf16_lo(xw[i]), bf16_hi(xw[i])));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) t[4 * u + i] = make_float2(0.f, 0.f);
-                    }
-                }
-                arrive(X_DONE + xb);
+                if (c == 0 && first) next_z(0);
+                __syncwarp();
                 wait(G_FULL + gs, c / NGR);
-                const float eg = gates[2 * gs + (one_head ? 0 : j)].eG[ln];
+                const Gates& G = gates[2 * gs + (ONE ? 0 : j)];
+                float e = G.pre[ln];
+                for (int b = 0; b < q; ++b) e += G.tot[b];
+                const float eg = ex2_approx(e);
                 arrive(G_FREE + gs);
-                wait(Y_FULL + j, 0);  // C h
+                wait(Y_FULL + j, 0);  // C h: times e^G, for W x to add to
                 __syncwarp();
                 tc::tc_after_sync();
-#pragma unroll
-                for (int n0 = 0; n0 < 64; n0 += 16) {
-                    float v[16];
-                    tc::tmem_ld16(ycol + n0, v);
+#pragma unroll 1
+                for (int n0 = 0; n0 < 64; n0 += 32) {
+                    float v[32];
+                    tc::tmem_ld32(ycol + n0, v);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2)
-                        t[(n0 + i) / 2] = __ffma2_rn(make_float2(eg, eg), make_float2(v[i], v[i + 1]), t[(n0 + i) / 2]);
-                }
-                tc::tc_before_sync();
-                arrive(Y_FREE + j);
-                wait(Y_FULL + j, 1);  // W x
-                __syncwarp();
-                tc::tc_after_sync();
+                    for (int k = 0; k < 32; k += 8) {
+                        uint32_t u[8];
 #pragma unroll
-                for (int n0 = 0; n0 < 64; n0 += 16) {
-                    float v[16];
-                    tc::tmem_ld16(ycol + n0, v);
-                    tc::tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2)
-                        t[(n0 + i) / 2] = __fadd2_rn(t[(n0 + i) / 2], make_float2(v[i], v[i + 1]));
-                }
-                tc::tc_before_sync();
-                arrive(Y_FREE + j);
-                // x is spent: its tile takes z, then y (each thread its own row)
-                wait(X_DONE + xb, xi / NXB);
-                if (a.z && hf.width) {
-                    if (first && !*abort_flag) {
-                        tc::mbar_arrive_expect_tx(&bars[Z_FULL + xb], K::TILE);
-                        tma_load_3d(base + K::OFF_X + xb * K::TILE, &p.z, hf.col, hf.head, row, &bars[Z_FULL + xb]);
-                        drain(&bars[Z_FULL + xb], (uint32_t)(xi / NXB) & 1u);
+                        for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(eg * v[k + i]);
+                        tc::tmem_st8(ycol + n0 + k, u);
                     }
-                    wait(Z_FULL + xb, xi / NXB);
                 }
+                tc::tmem_wait_st();
+                tc::tc_before_sync();
+                arrive(Y_FREE + j);
+                if (c > 0 && first) next_z(c);
+                __syncwarp();
+                wait(Y_FULL + j, 1);
+                wait(Z_FULL + j, c);
+                __syncwarp();
+                tc::tc_after_sync();
                 const bool whole = c * L + L <= rows;
                 bf* y = static_cast<bf*>(a.y) + ((int64_t)(row + ln) * a.H + hf.head) * a.P + hf.col;
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const uint32_t at = xrow + tc::sw128_off(ln, u);
+                // y takes z's place, each thread in its own row
+#pragma unroll 1
+                for (int n0 = 0; n0 < 64; n0 += 16) {
+                    float v[16];
+                    tc::tmem_ld16(ycol + n0, v);
+                    const uint32_t at[2] = {tile + tc::sw128_off(ln, n0 / 8), tile + tc::sw128_off(ln, n0 / 8 + 1)};
                     if (a.z) {
-                        const uint4 zu = tc::ld_shared_v4(at);
-                        const uint32_t zw[4] = {zu.x, zu.y, zu.z, zu.w};
+                        const uint4 z0 = tc::ld_shared_v4(at[0]), z1 = tc::ld_shared_v4(at[1]);
+                        const uint32_t zw[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+                        tc::tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            t[4 * u + i] = __fmul2_rn(t[4 * u + i], conv_silu2(make_float2(bf16_lo(zw[i]), bf16_hi(zw[i]))));
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 g = conv_silu2(make_float2(bf16_lo(zw[i]), bf16_hi(zw[i])));
+                            v[2 * i] *= g.x;
+                            v[2 * i + 1] *= g.y;
+                        }
+                    } else {
+                        tc::tmem_wait_ld();
                     }
-                    uint32_t ow[4];
+                    uint32_t ow[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) ow[i] = tc::pack_bf16(t[4 * u + i].x, t[4 * u + i].y);
-                    if (whole)
-                        tc::st_shared_v4(at, ow[0], ow[1], ow[2], ow[3]);
-                    else if (c * L + ln < rows && 8 * u < hf.width)  // rows behind belong to others
-                        *reinterpret_cast<uint4*>(y + 8 * u) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+                    for (int i = 0; i < 8; ++i) ow[i] = tc::pack_bf16(v[2 * i], v[2 * i + 1]);
+                    if (whole) {
+                        tc::st_shared_v4(at[0], ow[0], ow[1], ow[2], ow[3]);
+                        tc::st_shared_v4(at[1], ow[4], ow[5], ow[6], ow[7]);
+                    } else if (c * L + ln < rows && n0 < hf.width) {  // rows behind belong to others
+                        *reinterpret_cast<uint4*>(y + n0) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+                        *reinterpret_cast<uint4*>(y + n0 + 8) = make_uint4(ow[4], ow[5], ow[6], ow[7]);
+                    }
                 }
+                tc::tc_before_sync();
+                arrive(Y_FREE + j);
                 tc::fence_async_smem();
                 tc::named_bar(2 + j, 128);
-                if (first) {
-                    if (whole && hf.width && !*abort_flag) {
-                        tma_store_3d(&p.y, xrow, hf.col, hf.head, row);
-                        tc::bulk_commit();
-                        tc::bulk_wait_read0();
-                    }
-                    tc::mbar_arrive(&bars[X_FREE + xb]);
+                if (first && whole && hf.width && !*abort_flag) {
+                    tma_store_3d(&p.y, tile, hf.col, hf.head, row);
+                    tc::bulk_commit();
                 }
                 __syncwarp();
             }
-            if (first) tc::bulk_wait0();  // y is in global memory before the CTA leaves
+            if (first) {  // never leave with a copy in flight; y is in global memory
+                tc::bulk_wait0();
+                if (nch > 0) drain(&bars[Z_FULL + j], (uint32_t)(nch - 1) & 1u);
+            }
         }
     } else if (warp < 26) {
         // ============================================================ gate warps
-        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int j = warp - 24;
         const Half hf = half_of(p, unit, j);
-        const bool on = hf.width > 0 && !(one_head && j == 1);
+        const bool on = hf.width > 0 && !(ONE && j == 1);
         const float A2 = on ? -expf(a.A_log[hf.head]) * tcf::kLog2e : 0.f;
         const float bias = on ? a.dt_bias[hf.head] : 0.f;
         const __nv_bfloat16* dtp = static_cast<const __nv_bfloat16*>(a.dt) + hf.head;
-        float raw[4];
+        float raw[4];  // four tokens a lane
         auto fetch = [&](int c) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int64_t t = (int64_t)c * L + 4 * lane + i;
+                const int t = c * L + 4 * lane + i;
                 raw[i] = on && t < rows ? __bfloat162float(dtp[(r0 + t) * a.dts]) : 0.f;
             }
         };
@@ -629,15 +633,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             float d[4], g[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const bool in = on && c * (int64_t)L + 4 * lane + i < rows;
+                const bool in = on && c * L + 4 * lane + i < rows;
                 d[i] = in ? softplus_f32(raw[i] + bias) : 0.f;
-                // (written so that a NaN stays one)
                 g[i] = d[i] * A2;
-                g[i] = g[i] < kMinG2 ? kMinG2 : g[i];
+                g[i] = g[i] < kMinG2 ? kMinG2 : g[i];  // (written so that a NaN stays one)
             }
             if (c + 1 < nch) fetch(c + 1);
-            // inclusive sums within the block of 32 tokens (8 lanes), from the left
-            // and, of the tokens behind, from the right
+            // sums within the block of 32 tokens (8 lanes), from both ends
             const float sum = (g[0] + g[1]) + (g[2] + g[3]);
             float left = sum, right = sum;
 #pragma unroll
@@ -649,15 +651,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             float before = __shfl_up_sync(0xffffffffu, left, 1), behind = __shfl_down_sync(0xffffffffu, right, 1);
             if ((lane & 7) == 0) before = 0.f;
             if ((lane & 7) == 7) behind = 0.f;
-            float tot[4];
+            float tot[4], later = 0.f;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) tot[b] = __shfl_sync(0xffffffffu, left, 8 * b + 7);
-            const int blk = lane >> 3;
-            float earlier = 0.f, later = 0.f;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (b < blk) earlier += tot[b];
-                if (b > blk) later += tot[b];
+            for (int b = 3; b >= 0; --b) {
+                tot[b] = __shfl_sync(0xffffffffu, left, 8 * b + 7);
+                if (b > lane >> 3) later += tot[b];
             }
             const float p0 = before + g[0], p1 = p0 + g[1], p2 = p1 + g[2], p3 = p2 + g[3];
             const float s3 = behind, s2 = s3 + g[3], s1 = s2 + g[2], s0 = s1 + g[1];
@@ -673,11 +671,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             *reinterpret_cast<float4*>(&G.w[t]) =
                 make_float4(d[0] * exp2f(s0 + later), d[1] * exp2f(s1 + later), d[2] * exp2f(s2 + later),
                             d[3] * exp2f(s3 + later));
-            *reinterpret_cast<float4*>(&G.eG[t]) =
-                make_float4(exp2f(p0 + earlier), exp2f(p1 + earlier), exp2f(p2 + earlier), exp2f(p3 + earlier));
-            if (lane < 4) G.tot[lane] = lane == 0 ? tot[0] : (lane == 1 ? tot[1] : (lane == 2 ? tot[2] : tot[3]));
-            if (lane == 4) {
-                const float all = (tot[0] + tot[1]) + (tot[2] + tot[3]);
+            if (lane == 0) {
+                *reinterpret_cast<float4*>(G.tot) = make_float4(tot[0], tot[1], tot[2], tot[3]);
+                const float all = later + tot[0];
                 G.lastg = all;
                 G.last = exp2f(all);
             }
@@ -685,7 +681,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         }
     } else if (warp == 26) {
         // ============================================================== TMA warp
-        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (lane == 0) {
             Half hf[2] = {half_of(p, unit, 0), half_of(p, unit, 1)};
             // a missing second head reads the first one's columns: nothing uses them
@@ -695,7 +690,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 const int r = (int)(r0 + (int64_t)c * L), st = c & 1;
                 for (int j = 0; j < 2; ++j) {
                     const int xi = 2 * c + j, xb = xi % NXB;
-                    if (xi >= NXB) wait((STATES ? X_DONE : X_FREE) + xb, xi / NXB - 1);
+                    if (xi >= NXB) wait(X_DONE + xb, xi / NXB - 1);
                     tc::mbar_arrive_expect_tx(&bars[X_FULL + xb], K::TILE);
                     tma_load_3d(base + K::OFF_X + xb * K::TILE, &p.x, hf[j].col, hf[j].head, r, &bars[X_FULL + xb]);
                 }
@@ -719,7 +714,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         }
     } else {
         // ============================================================== MMA warp
-        if constexpr (!STATES) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         constexpr uint32_t idCB = tc::idesc_bf16(128, 128, 0, 0),
                            idY1 = tc::idesc_bf16(128, 64, 0, 1), idS = tc::idesc_bf16(128, NP, 0, 1);
         auto ready = [&](int b, int phase) {
@@ -773,12 +767,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             ready(Y_FREE + j, 0);
             if (tc::elect_one()) {
                 const uint32_t lx = tc::desc_lo(sbase + K::OFF_X + xb * K::TILE, K::TILE);
-                const uint32_t w = tmem + K::COL_CB + (one_head ? 0 : 16 * j);
+                const uint32_t w = tmem + K::COL_CB + (ONE ? 0 : 8 * j);
                 const uint32_t d = tmem + K::COL_Y + 64 * j;
-                tc::mma_ts<0>(d, w, tc::desc(lx), idY1);
+                tc::mma_ts<1>(d, w, tc::desc(lx), idY1);
 #pragma unroll
                 for (int k = 1; k < 8; ++k)
-                    tc::mma_ts<1>(d, w + 32 * (k >> 1) + 8 * (k & 1), tc::desc(lx + 128 * k), idY1);
+                    tc::mma_ts<1>(d, w + 16 * k, tc::desc(lx + 128 * k), idY1);
                 tc::mma_commit(&bars[Y_FULL + j]);
                 tc::mma_commit(&bars[X_DONE + xb]);
                 if (j == 1) tc::mma_commit(&bars[W_FREE]);
@@ -803,8 +797,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             }
             __syncwarp();
         };
-        // Per chunk: C B^T, then C h and the state's products, under which the M warps make
-        // W; then W x, under which the S warps hand over the next chunk's state.
+        // Per chunk: C B^T; the state's products and C h, under which the M warps make W and
+        // the Y warps write out the last chunk; then W x, under which the S warps hand over
+        // the next chunk's state.
         for (int c = 0; c < nch; ++c) {
             if constexpr (STATES) {
                 ready(B_FULL + (c & 1), c >> 1);
@@ -813,8 +808,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             } else {
                 issue_cb(c);
                 ready(S_READY, c);
-                issue_y2(c);
                 for (int k = 0; k < 4; ++k) issue_s(c, k);
+                issue_y2(c);
                 ready(M_FULL, c);
                 issue_y1(c, 0);
                 issue_y1(c, 1);
@@ -945,17 +940,19 @@ inline bool tma_rows(const void* t, int64_t stride) {
 template <int NP>
 inline cudaError_t launch_scan_np(const ScanTcArgs& p, const ScanPlan& r, cudaStream_t st) {
     using K = ScanCfg<NP>;
-    cudaError_t e = cudaFuncSetAttribute(scan_tc_kernel<NP, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::SMEM);
+    auto main = p.a.P == 128 ? scan_tc_kernel<NP, false, true> : scan_tc_kernel<NP, false, false>;
+    auto states = p.a.P == 128 ? scan_tc_kernel<NP, true, true> : scan_tc_kernel<NP, true, false>;
+    cudaError_t e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::SMEM);
     if (e != cudaSuccess) return e;
     if (r.slots > 0) {
-        e = cudaFuncSetAttribute(scan_tc_kernel<NP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::SMEM);
+        e = cudaFuncSetAttribute(states, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::SMEM);
         if (e != cudaSuccess) return e;
-        scan_tc_kernel<NP, true><<<(unsigned)(r.slots * r.units), kScanThreads, K::SMEM, st>>>(p);
+        states<<<(unsigned)(r.slots * r.units), kScanThreads, K::SMEM, st>>>(p);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         scan_chain_kernel<<<dim3((unsigned)(p.a.N / 2), (unsigned)r.units, (unsigned)p.a.n_seq), 256, 0, st>>>(p);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    scan_tc_kernel<NP, false><<<(unsigned)(r.segments * r.units), kScanThreads, K::SMEM, st>>>(p);
+    main<<<(unsigned)(r.segments * r.units), kScanThreads, K::SMEM, st>>>(p);
     return cudaGetLastError();
 }
 
