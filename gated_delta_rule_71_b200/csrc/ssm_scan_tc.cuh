@@ -71,9 +71,9 @@ struct ScanCfg {
     static constexpr int NH = NP / 64;
     static constexpr uint32_t TILE = 16384;             // 128 rows of 128 bytes
     static constexpr uint32_t BT = NH * TILE;
-    static constexpr uint32_t OFF_B = 0;                // [2]
-    static constexpr uint32_t OFF_C = OFF_B + 2 * BT;
-    static constexpr uint32_t OFF_X = OFF_C + BT;       // [NXB]
+    static constexpr uint32_t OFF_B = 0;
+    static constexpr uint32_t OFF_C = OFF_B + BT;       // [2]
+    static constexpr uint32_t OFF_X = OFF_C + 2 * BT;   // [NXB]
     static constexpr uint32_t OFF_Z = OFF_X + NXB * TILE;  // [2 halves] z, then y in its place
     static constexpr uint32_t OFF_H = OFF_Z + 2 * TILE;
     static constexpr uint32_t OFF_G = OFF_H + BT;       // [NGR][2] Gates
@@ -89,10 +89,10 @@ struct ScanCfg {
 };
 
 enum : int {
-    B_FULL = 0, B_FREE = B_FULL + 2, C_FULL_ = B_FREE + 2, C_FREE_, X_FULL, X_DONE = X_FULL + NXB,
+    B_FULL = 0, B_FREE, C_FULL_, C_FREE_ = C_FULL_ + 2, X_FULL = C_FREE_ + 2, X_DONE = X_FULL + NXB,
     Z_FULL = X_DONE + NXB, G_FULL = Z_FULL + 2, G_FREE = G_FULL + NGR, CB_FULL = G_FREE + NGR, M_FULL, W_FREE,
     XQ_FULL, XQ_FREE = XQ_FULL + 2, S_READY = XQ_FREE + 2, DS_DONE, H_FREE, Y_FULL, Y_FREE = Y_FULL + 2,
-    CLEAN = Y_FREE + 2, S_DRAIN, N_SCAN_BARS
+    CLEAN = Y_FREE + 2, S_DRAIN, N_SCAN_BARS = S_DRAIN + 2
 };
 static_assert(N_SCAN_BARS <= 52, "barrier slots");
 
@@ -136,6 +136,12 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t* r) {
 __device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
@@ -234,8 +240,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         for (int i = 0; i < N_SCAN_BARS; ++i) {
             uint32_t n = 1;
             if (i >= X_DONE && i < X_DONE + NXB) n = STATES ? 4 : 3;  // X warps (, the product)
-            if (i >= G_FULL && i < G_FULL + NGR) n = 2;
-            if (i >= G_FREE && i < G_FREE + NGR) n = STATES ? 12 : 24;
+            if (i == B_FREE) n = STATES ? 1 : 2;  // the products of two warps
+            if (i >= G_FULL && i < G_FULL + NGR) n = 4;
+            if (i >= G_FREE && i < G_FREE + NGR) n = STATES ? 8 : 20;
             if (i == M_FULL) n = 8;
             if (i == XQ_FULL || i == XQ_FULL + 1 || i == S_READY || i == Y_FREE ||
                 i == Y_FREE + 1 || i == CLEAN)
@@ -278,14 +285,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 // rows behind the sequence's end belong to another one: x and B to zero
                 // (a zero weight would still carry a NaN through the products)
                 for (int h = 0; h < 2; ++h) wait(X_FULL + (2 * c + h) % NXB, (2 * c + h) / NXB);
-                wait(B_FULL + (c & 1), c >> 1);
+                wait(B_FULL, c);
                 if (ln >= tail) {
                     const uint32_t row = (uint32_t)ln * 128u;
                     for (int i = 0; i < 8; ++i) {
                         for (int h = 0; h < 2; ++h)
                             tc::st_shared_v4(sbase + K::OFF_X + ((2 * c + h) % NXB) * K::TILE + row + 16 * i, 0, 0, 0, 0);
                         for (int h = 0; h < NH; ++h)
-                            tc::st_shared_v4(sbase + K::OFF_B + (c & 1) * K::BT + h * K::TILE + row + 16 * i, 0, 0, 0, 0);
+                            tc::st_shared_v4(sbase + K::OFF_B + h * K::TILE + row + 16 * i, 0, 0, 0, 0);
                     }
                 }
                 tc::fence_async_smem();
@@ -448,6 +455,79 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             tc::tmem_st16(lane_base + K::COL_S + n0, u);
         }
         tc::tmem_wait_st();
+        // The gates are made here too, two chunks ahead, while the products run: a token a
+        // thread, a block of 32 tokens a warp.
+        constexpr int HEADS = ONE ? 1 : 2;
+        bool on[HEADS];
+        float A2[HEADS], bias[HEADS];
+        uint16_t raw[HEADS];
+#pragma unroll
+        for (int h = 0; h < HEADS; ++h) {
+            const Half f = half_of(p, unit, h);
+            on[h] = f.width > 0;
+            A2[h] = on[h] ? -expf(a.A_log[f.head]) * tcf::kLog2e : 0.f;
+            bias[h] = on[h] ? a.dt_bias[f.head] : 0.f;
+            raw[h] = 0;
+        }
+        const uint16_t* dtp = static_cast<const uint16_t*>(a.dt) + (r0 + ln) * a.dts + half_of(p, unit, 0).head;
+        auto fetch = [&](int c) {
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h)
+                if (on[h] && c * L + ln < rows) raw[h] = dtp[(int64_t)c * L * a.dts + h];
+        };
+        auto make_gates = [&](int c) {
+            const int gs = c % NGR;
+            Gates* G = &gates[2 * gs];
+            float d[HEADS], left[HEADS], right[HEADS], behind[HEADS];
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h) {
+                const float v = __uint_as_float((uint32_t)raw[h] << 16) + bias[h];
+                d[h] = on[h] && c * L + ln < rows ? softplus_f32(v) : 0.f;
+                float g = d[h] * A2[h];
+                g = g < kMinG2 ? kMinG2 : g;  // (written so that a NaN stays one)
+                left[h] = right[h] = g;
+            }
+            if (c + 1 < nch) fetch(c + 1);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1)  // sums within the block, from both ends
+#pragma unroll
+                for (int h = 0; h < HEADS; ++h) {
+                    const float u = __shfl_up_sync(0xffffffffu, left[h], o), v = __shfl_down_sync(0xffffffffu, right[h], o);
+                    if (lane >= o) left[h] += u;
+                    if (lane + o < 32) right[h] += v;
+                }
+            if (c >= NGR) wait(G_FREE + gs, c / NGR - 1);
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h) {
+                behind[h] = __shfl_down_sync(0xffffffffu, right[h], 1);
+                if (lane == 31) {
+                    behind[h] = 0.f;
+                    G[h].tot[q] = left[h];
+                }
+                G[h].pre[ln] = left[h];
+                // (the weights of W are rounded to bf16: approximate exponentials do)
+                G[h].prd[ln] = __log2f(d[h]) - left[h];
+                G[h].col[ln] = d[h] * ex2_approx(behind[h]);
+            }
+            tc::named_bar(4, 128);
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h) {
+                float later = 0.f;
+                for (int b = 3; b > q; --b) later += G[h].tot[b];
+                G[h].w[ln] = d[h] * exp2f(behind[h] + later);
+                if (ln == 0) {
+                    const float all = later + G[h].tot[0];
+                    G[h].lastg = all;
+                    G[h].last = exp2f(all);
+                }
+            }
+            arrive(G_FULL + gs);
+        };
+        if (nch > 0) {
+            fetch(0);
+            make_gates(0);
+        }
+        if (nch > 1) make_gates(1);
         float sum_g = 0.f;
         for (int c = 0; c < nch; ++c) {
             const int gs = c % NGR;
@@ -482,7 +562,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             tc::fence_async_smem();
             tc::tc_before_sync();
             arrive(S_READY);
-            arrive(G_FREE + gs);
+            if (c + 2 < nch) make_gates(c + 2);
         }
         // the state that leaves it
         if (nch > 0) wait(DS_DONE, nch - 1);
@@ -611,74 +691,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 if (nch > 0) drain(&bars[Z_FULL + j], (uint32_t)(nch - 1) & 1u);
             }
         }
-    } else if (warp < 26) {
-        // ============================================================ gate warps
-        const int j = warp - 24;
-        const Half hf = half_of(p, unit, j);
-        const bool on = hf.width > 0 && !(ONE && j == 1);
-        const float A2 = on ? -expf(a.A_log[hf.head]) * tcf::kLog2e : 0.f;
-        const float bias = on ? a.dt_bias[hf.head] : 0.f;
-        const __nv_bfloat16* dtp = static_cast<const __nv_bfloat16*>(a.dt) + hf.head;
-        float raw[4];  // four tokens a lane
-        auto fetch = [&](int c) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = c * L + 4 * lane + i;
-                raw[i] = on && t < rows ? __bfloat162float(dtp[(r0 + t) * a.dts]) : 0.f;
-            }
-        };
-        if (nch > 0) fetch(0);
-        for (int c = 0; c < nch; ++c) {
-            const int gs = c % NGR;
-            float d[4], g[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool in = on && c * L + 4 * lane + i < rows;
-                d[i] = in ? softplus_f32(raw[i] + bias) : 0.f;
-                g[i] = d[i] * A2;
-                g[i] = g[i] < kMinG2 ? kMinG2 : g[i];  // (written so that a NaN stays one)
-            }
-            if (c + 1 < nch) fetch(c + 1);
-            // sums within the block of 32 tokens (8 lanes), from both ends
-            const float sum = (g[0] + g[1]) + (g[2] + g[3]);
-            float left = sum, right = sum;
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                const float u = __shfl_up_sync(0xffffffffu, left, o), v = __shfl_down_sync(0xffffffffu, right, o);
-                if ((lane & 7) >= o) left += u;
-                if ((lane & 7) + o < 8) right += v;
-            }
-            float before = __shfl_up_sync(0xffffffffu, left, 1), behind = __shfl_down_sync(0xffffffffu, right, 1);
-            if ((lane & 7) == 0) before = 0.f;
-            if ((lane & 7) == 7) behind = 0.f;
-            float tot[4], later = 0.f;
-#pragma unroll
-            for (int b = 3; b >= 0; --b) {
-                tot[b] = __shfl_sync(0xffffffffu, left, 8 * b + 7);
-                if (b > lane >> 3) later += tot[b];
-            }
-            const float p0 = before + g[0], p1 = p0 + g[1], p2 = p1 + g[2], p3 = p2 + g[3];
-            const float s3 = behind, s2 = s3 + g[3], s1 = s2 + g[2], s0 = s1 + g[1];
-            if (c >= NGR) wait(G_FREE + gs, c / NGR - 1);
-            __syncwarp();
-            Gates& G = gates[2 * gs + j];
-            const int t = 4 * lane;
-            *reinterpret_cast<float4*>(&G.pre[t]) = make_float4(p0, p1, p2, p3);
-            *reinterpret_cast<float4*>(&G.prd[t]) =
-                make_float4(log2f(d[0]) - p0, log2f(d[1]) - p1, log2f(d[2]) - p2, log2f(d[3]) - p3);
-            *reinterpret_cast<float4*>(&G.col[t]) =
-                make_float4(d[0] * exp2f(s0), d[1] * exp2f(s1), d[2] * exp2f(s2), d[3] * exp2f(s3));
-            *reinterpret_cast<float4*>(&G.w[t]) =
-                make_float4(d[0] * exp2f(s0 + later), d[1] * exp2f(s1 + later), d[2] * exp2f(s2 + later),
-                            d[3] * exp2f(s3 + later));
-            if (lane == 0) {
-                *reinterpret_cast<float4*>(G.tot) = make_float4(tot[0], tot[1], tot[2], tot[3]);
-                const float all = later + tot[0];
-                G.lastg = all;
-                G.last = exp2f(all);
-            }
-            arrive(G_FULL + gs);
-        }
     } else if (warp == 26) {
         // ============================================================== TMA warp
         if (lane == 0) {
@@ -694,130 +706,126 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                     tc::mbar_arrive_expect_tx(&bars[X_FULL + xb], K::TILE);
                     tma_load_3d(base + K::OFF_X + xb * K::TILE, &p.x, hf[j].col, hf[j].head, r, &bars[X_FULL + xb]);
                 }
-                if (c >= 2) wait(B_FREE + st, (c >> 1) - 1);
-                tc::mbar_arrive_expect_tx(&bars[B_FULL + st], K::BT);
+                if (c >= 1) wait(B_FREE, c - 1);
+                tc::mbar_arrive_expect_tx(&bars[B_FULL], K::BT);
                 for (int h = 0; h < NH; ++h)
-                    tma_load_3d(base + K::OFF_B + st * K::BT + h * K::TILE, &p.b, 64 * h, grp, r, &bars[B_FULL + st]);
+                    tma_load_3d(base + K::OFF_B + h * K::TILE, &p.b, 64 * h, grp, r, &bars[B_FULL]);
+                if (c + 1 < nch)  // its one buffer is refilled late: from L2 then
+                    for (int h = 0; h < NH; ++h) tma_prefetch_3d(&p.b, 64 * h, grp, r + L);
                 if (!STATES) {
-                    if (c >= 1) wait(C_FREE_, c - 1);
-                    tc::mbar_arrive_expect_tx(&bars[C_FULL_], K::BT);
+                    if (c >= 2) wait(C_FREE_ + st, (c >> 1) - 1);
+                    tc::mbar_arrive_expect_tx(&bars[C_FULL_ + st], K::BT);
                     for (int h = 0; h < NH; ++h)
-                        tma_load_3d(base + K::OFF_C + h * K::TILE, &p.c, 64 * h, grp, r, &bars[C_FULL_]);
+                        tma_load_3d(base + K::OFF_C + st * K::BT + h * K::TILE, &p.c, 64 * h, grp, r, &bars[C_FULL_ + st]);
                 }
                 done = c + 1;
             }
             // never leave with a copy in flight
-            for (int c = done >= 2 ? done - 2 : 0; c < done; ++c) drain(&bars[B_FULL + (c & 1)], (c >> 1) & 1);
-            if (!STATES && done > 0) drain(&bars[C_FULL_], (done - 1) & 1);
+            if (done > 0) drain(&bars[B_FULL], (done - 1) & 1);
+            for (int c = done >= 2 ? done - 2 : 0; !STATES && c < done; ++c) drain(&bars[C_FULL_ + (c & 1)], (c >> 1) & 1);
             for (int i = 2 * done >= NXB ? 2 * done - NXB : 0; i < 2 * done; ++i)
                 drain(&bars[X_FULL + i % NXB], (i / NXB) & 1);
         }
-    } else {
-        // ============================================================== MMA warp
-        constexpr uint32_t idCB = tc::idesc_bf16(128, 128, 0, 0),
-                           idY1 = tc::idesc_bf16(128, 64, 0, 1), idS = tc::idesc_bf16(128, NP, 0, 1);
-        auto ready = [&](int b, int phase) {
-            tcf::wait_warp(&bars[b], (uint32_t)phase & 1u, abort_flag);
+    } else if (warp < 26) {
+        // ============================================================= MMA warps
+        // Warp 25 the state's products; warp 24 C B^T, C h and W x.  Two warps, since one
+        // would issue a chunk's 50 products slower than the tensor cores run them.
+        constexpr uint32_t idCB = tc::idesc_bf16(128, 128, 0, 0), idY1 = tc::idesc_bf16(128, 64, 0, 1),
+                           idS = tc::idesc_bf16(128, NP, 0, 1);
+        auto ready = [&](int b, int phase) { tcf::wait_warp(&bars[b], (uint32_t)phase & 1u, abort_flag); };
+        auto go = [&]() {
             __syncwarp();
             tc::tc_after_sync();
         };
-        // one quarter of S += (w x)^T B, 32 tokens
-        auto issue_s = [&](int c, int k) {
-            const int it = 4 * c + k, buf = it & 1;
-            ready(XQ_FULL + buf, it >> 1);
-            if (tc::elect_one()) {
-                const uint32_t lb = tc::desc_lo(sbase + K::OFF_B + (c & 1) * K::BT, K::TILE);
-#pragma unroll
-                for (int s = 0; s < 3; ++s)
-#pragma unroll
-                    for (int ks = 0; ks < 2; ++ks)
-                        tc::mma_ts<1>(tmem + K::COL_S, tmem + K::COL_WX + 48 * buf + 16 * s + 8 * ks,
-                                      tc::desc(lb + 128 * (2 * k + ks)), idS);
-                tc::mma_commit(&bars[XQ_FREE + buf]);
-                if (k == 3) {
-                    tc::mma_commit(&bars[DS_DONE]);
-                    tc::mma_commit(&bars[B_FREE + (c & 1)]);
-                }
-            }
-            __syncwarp();
-        };
-        auto issue_y2 = [&](int c) {
-            if (c > 0) {
-                ready(Y_FREE, 1);
-                ready(Y_FREE + 1, 1);
-            }
-            if (tc::elect_one()) {
-                const uint32_t lc = tc::desc_lo(sbase + K::OFF_C, 16), lh = tc::desc_lo(sbase + K::OFF_H, 16);
-                tc::mma_ss<0>(tmem + K::COL_Y, tc::desc(lc), tc::desc(lh), idCB);
-#pragma unroll
-                for (int k = 1; k < NP / 16; ++k) {
-                    const uint32_t o = (k >> 2) * (K::TILE / 16) + (k & 3) * 2;
-                    tc::mma_ss<1>(tmem + K::COL_Y, tc::desc(lc + o), tc::desc(lh + o), idCB);
-                }
-                tc::mma_commit(&bars[Y_FULL]);
-                tc::mma_commit(&bars[Y_FULL + 1]);
-                tc::mma_commit(&bars[H_FREE]);
-                tc::mma_commit(&bars[C_FREE_]);
-            }
-            __syncwarp();
-        };
-        auto issue_y1 = [&](int c, int j) {
-            const int xi = 2 * c + j, xb = xi % NXB;
-            ready(X_FULL + xb, xi / NXB);
-            ready(Y_FREE + j, 0);
-            if (tc::elect_one()) {
-                const uint32_t lx = tc::desc_lo(sbase + K::OFF_X + xb * K::TILE, K::TILE);
-                const uint32_t w = tmem + K::COL_CB + (ONE ? 0 : 8 * j);
-                const uint32_t d = tmem + K::COL_Y + 64 * j;
-                tc::mma_ts<1>(d, w, tc::desc(lx), idY1);
-#pragma unroll
-                for (int k = 1; k < 8; ++k)
-                    tc::mma_ts<1>(d, w + 16 * k, tc::desc(lx + 128 * k), idY1);
-                tc::mma_commit(&bars[Y_FULL + j]);
-                tc::mma_commit(&bars[X_DONE + xb]);
-                if (j == 1) tc::mma_commit(&bars[W_FREE]);
-            }
-            __syncwarp();
-        };
-        auto issue_cb = [&](int c) {
-            ready(B_FULL + (c & 1), c >> 1);
-            if (c == nch - 1 && tail < L) ready(CLEAN, 0);
-            ready(C_FULL_, c);
-            if (c > 0) ready(W_FREE, c - 1);  // the last chunk's W has been read
-            if (tc::elect_one()) {
-                const uint32_t lc = tc::desc_lo(sbase + K::OFF_C, 16),
-                               lb = tc::desc_lo(sbase + K::OFF_B + (c & 1) * K::BT, 16);
-                tc::mma_ss<0>(tmem + K::COL_CB, tc::desc(lc), tc::desc(lb), idCB);
-#pragma unroll
-                for (int k = 1; k < NP / 16; ++k) {
-                    const uint32_t o = (k >> 2) * (K::TILE / 16) + (k & 3) * 2;
-                    tc::mma_ss<1>(tmem + K::COL_CB, tc::desc(lc + o), tc::desc(lb + o), idCB);
-                }
-                tc::mma_commit(&bars[CB_FULL]);
-            }
-            __syncwarp();
-        };
-        // Per chunk: C B^T; the state's products and C h, under which the M warps make W and
-        // the Y warps write out the last chunk; then W x, under which the S warps hand over
-        // the next chunk's state.
-        for (int c = 0; c < nch; ++c) {
-            if constexpr (STATES) {
-                ready(B_FULL + (c & 1), c >> 1);
+        const uint32_t lb0 = tc::desc_lo(sbase + K::OFF_B, K::TILE), lbk = tc::desc_lo(sbase + K::OFF_B, 16);
+        if (warp == 25) {
+            for (int c = 0; c < nch; ++c) {
+                ready(B_FULL, c);
+                if (c == nch - 1 && tail < L) ready(CLEAN, 0);
                 ready(S_READY, c);
-                for (int k = 0; k < 4; ++k) issue_s(c, k);
-            } else {
-                issue_cb(c);
+                for (int k = 0; k < 4; ++k) {  // S += (w x)^T B, 32 tokens
+                    const int buf = k & 1;
+                    ready(XQ_FULL + buf, 2 * c + (k >> 1));
+                    go();
+                    if (tc::elect_one()) {
+                        const uint32_t wx = tmem + K::COL_WX + 48 * buf, lb = lb0 + 256 * k;
+#pragma unroll
+                        for (int s = 0; s < 3; ++s)
+#pragma unroll
+                            for (int ks = 0; ks < 2; ++ks)
+                                tc::mma_ts<1>(tmem + K::COL_S, wx + 16 * s + 8 * ks, tc::desc(lb + 128 * ks), idS);
+                        tc::mma_commit(&bars[XQ_FREE + buf]);
+                        if (k == 3) {
+                            tc::mma_commit(&bars[DS_DONE]);
+                            tc::mma_commit(&bars[B_FREE]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        } else if constexpr (!STATES) {
+            for (int c = 0; c < nch; ++c) {
+                const uint32_t lc = tc::desc_lo(sbase + K::OFF_C + (c & 1) * K::BT, 16);
+                ready(B_FULL, c);
+                if (c == nch - 1 && tail < L) ready(CLEAN, 0);
+                ready(C_FULL_ + (c & 1), c >> 1);
+                if (c > 0) ready(W_FREE, c - 1);  // the last chunk's W has been read
+                go();
+                if (tc::elect_one()) {
+                    tc::mma_ss<0>(tmem + K::COL_CB, tc::desc(lc), tc::desc(lbk), idCB);
+#pragma unroll
+                    for (int k = 1; k < NP / 16; ++k) {
+                        const uint32_t o = (k >> 2) * (K::TILE / 16) + (k & 3) * 2;
+                        tc::mma_ss<1>(tmem + K::COL_CB, tc::desc(lc + o), tc::desc(lbk + o), idCB);
+                    }
+                    tc::mma_commit(&bars[CB_FULL]);
+                    tc::mma_commit(&bars[B_FREE]);
+                }
+                __syncwarp();
                 ready(S_READY, c);
-                for (int k = 0; k < 4; ++k) issue_s(c, k);
-                issue_y2(c);
+                if (c > 0) {
+                    ready(Y_FREE, 1);
+                    ready(Y_FREE + 1, 1);
+                }
+                go();
+                if (tc::elect_one()) {  // C h, both halves
+                    const uint32_t lh = tc::desc_lo(sbase + K::OFF_H, 16);
+                    tc::mma_ss<0>(tmem + K::COL_Y, tc::desc(lc), tc::desc(lh), idCB);
+#pragma unroll
+                    for (int k = 1; k < NP / 16; ++k) {
+                        const uint32_t o = (k >> 2) * (K::TILE / 16) + (k & 3) * 2;
+                        tc::mma_ss<1>(tmem + K::COL_Y, tc::desc(lc + o), tc::desc(lh + o), idCB);
+                    }
+                    tc::mma_commit(&bars[Y_FULL]);
+                    tc::mma_commit(&bars[Y_FULL + 1]);
+                    tc::mma_commit(&bars[H_FREE]);
+                    tc::mma_commit(&bars[C_FREE_ + (c & 1)]);
+                }
+                __syncwarp();
                 ready(M_FULL, c);
-                issue_y1(c, 0);
-                issue_y1(c, 1);
+#pragma unroll 1
+                for (int j = 0; j < 2; ++j) {  // W x, onto e^G C h
+                    const int xi = 2 * c + j, xb = xi % NXB;
+                    ready(X_FULL + xb, xi / NXB);
+                    ready(Y_FREE + j, 0);
+                    go();
+                    if (tc::elect_one()) {
+                        const uint32_t lx = tc::desc_lo(sbase + K::OFF_X + xb * K::TILE, K::TILE);
+                        const uint32_t w = tmem + K::COL_CB + (ONE ? 0 : 8 * j), d = tmem + K::COL_Y + 64 * j;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) tc::mma_ts<1>(d, w + 16 * k, tc::desc(lx + 128 * k), idY1);
+                        tc::mma_commit(&bars[Y_FULL + j]);
+                        tc::mma_commit(&bars[X_DONE + xb]);
+                        if (j == 1) tc::mma_commit(&bars[W_FREE]);
+                    }
+                    __syncwarp();
+                }
             }
         }
         if (tc::elect_one()) {  // never leave with a product in flight
-            tc::mma_commit(&bars[S_DRAIN]);
-            drain(&bars[S_DRAIN], 0);
+            uint64_t* bar = &bars[S_DRAIN + (warp & 1)];
+            tc::mma_commit(bar);
+            drain(bar, 0);
         }
         __syncwarp();
     }
