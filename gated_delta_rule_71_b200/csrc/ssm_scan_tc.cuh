@@ -42,7 +42,6 @@ namespace ssm {
 constexpr int L = 128;          // tokens of a chunk
 constexpr int kScanThreads = 896;
 constexpr int NGR = 3;          // gate ring
-constexpr int NXB = 3;          // half-tiles of x in flight
 constexpr float kMinG2 = -160.f;  // 2^-160 is 0 in fp32: more decay changes nothing
 
 struct Gates {                  // of one chunk and head; sums in log2 units
@@ -69,11 +68,15 @@ struct ScanTcArgs {
 template <int NP>
 struct ScanCfg {
     static constexpr int NH = NP / 64;
+    // tiles in flight: shared memory holds two of B and C at N <= 64, one at N = 128
+    // (refilled, from L2, under the products that do not need it)
+    static constexpr int NBC = NP == 128 ? 1 : 2;
+    static constexpr int NXB = NP == 128 ? 5 : 6;       // half-tiles of x
     static constexpr uint32_t TILE = 16384;             // 128 rows of 128 bytes
     static constexpr uint32_t BT = NH * TILE;
-    static constexpr uint32_t OFF_B = 0;
-    static constexpr uint32_t OFF_C = OFF_B + BT;       // [2]
-    static constexpr uint32_t OFF_X = OFF_C + 2 * BT;   // [NXB]
+    static constexpr uint32_t OFF_B = 0;                // [NBC]
+    static constexpr uint32_t OFF_C = OFF_B + NBC * BT; // [NBC]
+    static constexpr uint32_t OFF_X = OFF_C + NBC * BT; // [NXB]
     static constexpr uint32_t OFF_Z = OFF_X + NXB * TILE;  // [2 halves] z, then y in its place
     static constexpr uint32_t OFF_H = OFF_Z + 2 * TILE;
     static constexpr uint32_t OFF_G = OFF_H + BT;       // [NGR][2] Gates
@@ -89,8 +92,8 @@ struct ScanCfg {
 };
 
 enum : int {
-    B_FULL = 0, B_FREE, C_FULL_, C_FREE_ = C_FULL_ + 2, X_FULL = C_FREE_ + 2, X_DONE = X_FULL + NXB,
-    Z_FULL = X_DONE + NXB, G_FULL = Z_FULL + 2, G_FREE = G_FULL + NGR, CB_FULL = G_FREE + NGR, M_FULL, W_FREE,
+    B_FULL = 0, B_FREE = B_FULL + 2, C_FULL_ = B_FREE + 2, C_FREE_ = C_FULL_ + 2, X_FULL = C_FREE_ + 2,
+    X_DONE = X_FULL + 6, Z_FULL = X_DONE + 6, G_FULL = Z_FULL + 2, G_FREE = G_FULL + NGR, CB_FULL = G_FREE + NGR, M_FULL, W_FREE,
     XQ_FULL, XQ_FREE = XQ_FULL + 2, S_READY = XQ_FREE + 2, DS_DONE, H_FREE, Y_FULL, Y_FREE = Y_FULL + 2,
     CLEAN = Y_FREE + 2, S_DRAIN, N_SCAN_BARS = S_DRAIN + 2
 };
@@ -104,6 +107,32 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
+}
+// One poll that may sleep up to `ns` nanoseconds in hardware.  Most of the 28 warps wait
+// most of the time; short polls would take the issue slots and the shared-memory pipe
+// from the ones that work.
+__device__ __forceinline__ bool try_wait_ns(uint32_t bar, uint32_t phase, uint32_t ns) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(phase), "r"(ns)
+        : "memory");
+    return ok != 0;
+}
+constexpr uint32_t kNap = 20000, kNaps = 1u << 17;  // 20 us a poll, a few seconds in all
+__device__ __forceinline__ void nap_wait(uint64_t* bar, uint32_t phase, volatile uint32_t* abort) {
+    const uint32_t at = smem_u32(bar);
+    uint32_t i = 0;
+#pragma unroll 1
+    while (!try_wait_ns(at, phase, kNap)) {
+        if (*abort || ++i >= kNaps) {
+            *abort = 1u;
+            break;
+        }
+    }
 }
 // Bounded wait for what is still in flight on the way out (no abort flag).
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t phase) {
@@ -211,7 +240,7 @@ __device__ __forceinline__ Half half_of(const ScanTcArgs& p, int unit, int j) {
 template <int NP, bool STATES, bool ONE>
 __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_constant__ ScanTcArgs p) {
     using K = ScanCfg<NP>;
-    constexpr int NH = K::NH;
+    constexpr int NH = K::NH, NXB = K::NXB, NBC = K::NBC;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     const uint32_t sbase = (raw_u32 + 1023u) & ~1023u;
@@ -240,7 +269,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         for (int i = 0; i < N_SCAN_BARS; ++i) {
             uint32_t n = 1;
             if (i >= X_DONE && i < X_DONE + NXB) n = STATES ? 4 : 3;  // X warps (, the product)
-            if (i == B_FREE) n = STATES ? 1 : 2;  // the products of two warps
+            if (i == B_FREE || i == B_FREE + 1) n = STATES ? 1 : 2;  // the products of two warps
             if (i >= G_FULL && i < G_FULL + NGR) n = 4;
             if (i >= G_FREE && i < G_FREE + NGR) n = STATES ? 8 : 20;
             if (i == M_FULL) n = 8;
@@ -257,7 +286,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     __syncthreads();
     tc::tc_after_sync();
     const uint32_t tmem = __reduce_max_sync(0xffffffffu, misc[0]);
-    auto wait = [&](int b, int phase) { return tcf::wait(&bars[b], (uint32_t)phase & 1u, abort_flag); };
+    auto wait = [&](int b, int phase) { nap_wait(&bars[b], (uint32_t)phase & 1u, abort_flag); };
     auto arrive = [&](int b) {  // one arrival a warp
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bars[b]);
@@ -285,14 +314,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 // rows behind the sequence's end belong to another one: x and B to zero
                 // (a zero weight would still carry a NaN through the products)
                 for (int h = 0; h < 2; ++h) wait(X_FULL + (2 * c + h) % NXB, (2 * c + h) / NXB);
-                wait(B_FULL, c);
+                wait(B_FULL + c % NBC, c / NBC);
                 if (ln >= tail) {
                     const uint32_t row = (uint32_t)ln * 128u;
                     for (int i = 0; i < 8; ++i) {
                         for (int h = 0; h < 2; ++h)
                             tc::st_shared_v4(sbase + K::OFF_X + ((2 * c + h) % NXB) * K::TILE + row + 16 * i, 0, 0, 0, 0);
                         for (int h = 0; h < NH; ++h)
-                            tc::st_shared_v4(sbase + K::OFF_B + h * K::TILE + row + 16 * i, 0, 0, 0, 0);
+                            tc::st_shared_v4(sbase + K::OFF_B + (c % NBC) * K::BT + h * K::TILE + row + 16 * i, 0, 0, 0, 0);
                     }
                 }
                 tc::fence_async_smem();
@@ -699,30 +728,36 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             if (hf[1].width == 0) hf[1] = hf[0];
             int done = 0;
             for (int c = 0; c < nch && !*abort_flag; ++c) {
-                const int r = (int)(r0 + (int64_t)c * L), st = c & 1;
+                const int r = (int)(r0 + (int64_t)c * L);
                 for (int j = 0; j < 2; ++j) {
                     const int xi = 2 * c + j, xb = xi % NXB;
                     if (xi >= NXB) wait(X_DONE + xb, xi / NXB - 1);
                     tc::mbar_arrive_expect_tx(&bars[X_FULL + xb], K::TILE);
                     tma_load_3d(base + K::OFF_X + xb * K::TILE, &p.x, hf[j].col, hf[j].head, r, &bars[X_FULL + xb]);
                 }
-                if (c >= 1) wait(B_FREE, c - 1);
-                tc::mbar_arrive_expect_tx(&bars[B_FULL], K::BT);
-                for (int h = 0; h < NH; ++h)
-                    tma_load_3d(base + K::OFF_B + h * K::TILE, &p.b, 64 * h, grp, r, &bars[B_FULL]);
-                if (c + 1 < nch)  // its one buffer is refilled late: from L2 then
-                    for (int h = 0; h < NH; ++h) tma_prefetch_3d(&p.b, 64 * h, grp, r + L);
+                const int bc = c % NBC;
                 if (!STATES) {
-                    if (c >= 2) wait(C_FREE_ + st, (c >> 1) - 1);
-                    tc::mbar_arrive_expect_tx(&bars[C_FULL_ + st], K::BT);
+                    if (c >= NBC) wait(C_FREE_ + bc, c / NBC - 1);
+                    tc::mbar_arrive_expect_tx(&bars[C_FULL_ + bc], K::BT);
                     for (int h = 0; h < NH; ++h)
-                        tma_load_3d(base + K::OFF_C + st * K::BT + h * K::TILE, &p.c, 64 * h, grp, r, &bars[C_FULL_ + st]);
+                        tma_load_3d(base + K::OFF_C + bc * K::BT + h * K::TILE, &p.c, 64 * h, grp, r, &bars[C_FULL_ + bc]);
                 }
+                if (c >= NBC) wait(B_FREE + bc, c / NBC - 1);
+                tc::mbar_arrive_expect_tx(&bars[B_FULL + bc], K::BT);
+                for (int h = 0; h < NH; ++h)
+                    tma_load_3d(base + K::OFF_B + bc * K::BT + h * K::TILE, &p.b, 64 * h, grp, r, &bars[B_FULL + bc]);
+                if (NBC == 1 && c + 1 < nch)
+                    for (int h = 0; h < NH; ++h) {
+                        tma_prefetch_3d(&p.b, 64 * h, grp, r + L);
+                        if (!STATES) tma_prefetch_3d(&p.c, 64 * h, grp, r + L);
+                    }
                 done = c + 1;
             }
             // never leave with a copy in flight
-            if (done > 0) drain(&bars[B_FULL], (done - 1) & 1);
-            for (int c = done >= 2 ? done - 2 : 0; !STATES && c < done; ++c) drain(&bars[C_FULL_ + (c & 1)], (c >> 1) & 1);
+            for (int c = done >= NBC ? done - NBC : 0; c < done; ++c) {
+                drain(&bars[B_FULL + c % NBC], (c / NBC) & 1);
+                if (!STATES) drain(&bars[C_FULL_ + c % NBC], (c / NBC) & 1);
+            }
             for (int i = 2 * done >= NXB ? 2 * done - NXB : 0; i < 2 * done; ++i)
                 drain(&bars[X_FULL + i % NXB], (i / NXB) & 1);
         }
@@ -732,15 +767,15 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         // would issue a chunk's 50 products slower than the tensor cores run them.
         constexpr uint32_t idCB = tc::idesc_bf16(128, 128, 0, 0), idY1 = tc::idesc_bf16(128, 64, 0, 1),
                            idS = tc::idesc_bf16(128, NP, 0, 1);
-        auto ready = [&](int b, int phase) { tcf::wait_warp(&bars[b], (uint32_t)phase & 1u, abort_flag); };
+        auto ready = [&](int b, int phase) { nap_wait(&bars[b], (uint32_t)phase & 1u, abort_flag); };
         auto go = [&]() {
             __syncwarp();
             tc::tc_after_sync();
         };
-        const uint32_t lb0 = tc::desc_lo(sbase + K::OFF_B, K::TILE), lbk = tc::desc_lo(sbase + K::OFF_B, 16);
         if (warp == 25) {
             for (int c = 0; c < nch; ++c) {
-                ready(B_FULL, c);
+                const uint32_t lb0 = tc::desc_lo(sbase + K::OFF_B + (c % NBC) * K::BT, K::TILE);
+                ready(B_FULL + c % NBC, c / NBC);
                 if (c == nch - 1 && tail < L) ready(CLEAN, 0);
                 ready(S_READY, c);
                 for (int k = 0; k < 4; ++k) {  // S += (w x)^T B, 32 tokens
@@ -757,7 +792,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                         tc::mma_commit(&bars[XQ_FREE + buf]);
                         if (k == 3) {
                             tc::mma_commit(&bars[DS_DONE]);
-                            tc::mma_commit(&bars[B_FREE]);
+                            tc::mma_commit(&bars[B_FREE + c % NBC]);
                         }
                     }
                     __syncwarp();
@@ -765,10 +800,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             }
         } else if constexpr (!STATES) {
             for (int c = 0; c < nch; ++c) {
-                const uint32_t lc = tc::desc_lo(sbase + K::OFF_C + (c & 1) * K::BT, 16);
-                ready(B_FULL, c);
+                const int bc = c % NBC;
+                const uint32_t lc = tc::desc_lo(sbase + K::OFF_C + bc * K::BT, 16),
+                               lbk = tc::desc_lo(sbase + K::OFF_B + bc * K::BT, 16);
+                ready(B_FULL + bc, c / NBC);
                 if (c == nch - 1 && tail < L) ready(CLEAN, 0);
-                ready(C_FULL_ + (c & 1), c >> 1);
+                ready(C_FULL_ + bc, c / NBC);
                 if (c > 0) ready(W_FREE, c - 1);  // the last chunk's W has been read
                 go();
                 if (tc::elect_one()) {
@@ -779,7 +816,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                         tc::mma_ss<1>(tmem + K::COL_CB, tc::desc(lc + o), tc::desc(lbk + o), idCB);
                     }
                     tc::mma_commit(&bars[CB_FULL]);
-                    tc::mma_commit(&bars[B_FREE]);
+                    tc::mma_commit(&bars[B_FREE + bc]);
                 }
                 __syncwarp();
                 ready(S_READY, c);
@@ -799,7 +836,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                     tc::mma_commit(&bars[Y_FULL]);
                     tc::mma_commit(&bars[Y_FULL + 1]);
                     tc::mma_commit(&bars[H_FREE]);
-                    tc::mma_commit(&bars[C_FREE_ + (c & 1)]);
+                    tc::mma_commit(&bars[C_FREE_ + bc]);
                 }
                 __syncwarp();
                 ready(M_FULL, c);
