@@ -51,8 +51,7 @@ struct Gates {                  // of one chunk and head; sums in log2 units
     float prd[L];               // log2(dt) - pre
     float tot[4];               // block sums
     float last;                 // 2^(sum of the chunk)
-    float lastg;                // the chunk's sum itself
-    float pad[2];
+    float pad[3];
 };
 
 struct ScanTcArgs {
@@ -88,13 +87,14 @@ struct ScanCfg {
     static constexpr uint32_t COL_S = 128;              // S, lane = value lane, NP columns
     static constexpr uint32_t COL_Y = COL_S + NP;       // [2 halves] x 64
     static constexpr uint32_t COL_WX = COL_Y + 128;     // [2] x 48: three terms of 32 tokens
-    static_assert(COL_WX + 96 <= 512, "tensor memory budget");
+    static constexpr uint32_t COL_WX1 = COL_Y;          // [4] x 48 in the first pass
+    static_assert(COL_WX + 96 <= 512 && COL_WX1 + 192 <= 512, "tensor memory budget");
 };
 
 enum : int {
     B_FULL = 0, B_FREE = B_FULL + 2, C_FULL_ = B_FREE + 2, C_FREE_ = C_FULL_ + 2, X_FULL = C_FREE_ + 2,
-    X_DONE = X_FULL + 6, Z_FULL = X_DONE + 6, G_FULL = Z_FULL + 2, G_FREE = G_FULL + NGR, CB_FULL = G_FREE + NGR, M_FULL, W_FREE,
-    XQ_FULL, XQ_FREE = XQ_FULL + 2, S_READY = XQ_FREE + 2, DS_DONE, H_FREE, Y_FULL, Y_FREE = Y_FULL + 2,
+    X_DONE = X_FULL + 6, Z_FULL = X_DONE + 6, Y_OUT = Z_FULL + 2, G_FULL = Y_OUT + 2, G_FREE = G_FULL + NGR, CB_FULL = G_FREE + NGR, M_FULL, W_FREE,
+    XQ_FULL, XQ_FREE = XQ_FULL + 4, S_READY = XQ_FREE + 4, DS_DONE, H_FREE, Y_FULL, Y_FREE = Y_FULL + 2,
     CLEAN = Y_FREE + 2, S_DRAIN, N_SCAN_BARS = S_DRAIN + 2
 };
 static_assert(N_SCAN_BARS <= 52, "barrier slots");
@@ -268,12 +268,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     if (threadIdx.x == 0) {
         for (int i = 0; i < N_SCAN_BARS; ++i) {
             uint32_t n = 1;
-            if (i >= X_DONE && i < X_DONE + NXB) n = STATES ? 4 : 3;  // X warps (, the product)
+            if (i >= X_DONE && i < X_DONE + NXB) n = STATES ? 8 : 3;  // X warps (, the product)
             if (i == B_FREE || i == B_FREE + 1) n = STATES ? 1 : 2;  // the products of two warps
             if (i >= G_FULL && i < G_FULL + NGR) n = 4;
-            if (i >= G_FREE && i < G_FREE + NGR) n = STATES ? 8 : 20;
+            if (i >= G_FREE && i < G_FREE + NGR) n = STATES ? 16 : 20;
             if (i == M_FULL) n = 8;
-            if (i == XQ_FULL || i == XQ_FULL + 1 || i == S_READY || i == Y_FREE ||
+            if ((i >= XQ_FULL && i < XQ_FULL + 4) || i == S_READY || i == Y_OUT || i == Y_OUT + 1 || i == Y_FREE ||
                 i == Y_FREE + 1 || i == CLEAN)
                 n = 4;
             mbar_init(&bars[i], n);
@@ -292,16 +292,20 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         if (lane == 0) tc::mbar_arrive(&bars[b]);
     };
 
+    // The first pass walks a segment from its end, so that each token's weight reaches to
+    // the segment's end and the sum needs no decay between chunks: step c is chunk_of(c).
+    auto chunk_of = [&](int c) { return STATES ? nch - 1 - c : c; };
     const int q = warp & 3, ln = 32 * q + lane;  // tensor-memory lane of the four-warp jobs
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
 
-    if (warp < (STATES ? 8 : 4)) {
+    if (warp < 4 || (STATES && (warp < 12 || (warp >= 16 && warp < 20)))) {
         // =============================================================== X warps
         // A chunk goes through in quarters of 32 tokens and two buffers of tensor memory
-        // (the first pass has two warpgroups for it, a buffer each).  x^T comes out of
+        // (the first pass has a warpgroup and a buffer for each quarter).  x^T comes out of
         // shared memory by transposing 8 x 8 loads: a thread gets two tokens of a value
         // column, the layout in which 16 lanes x 4 columns go to tensor memory.
-        constexpr int SETS = STATES ? 2 : 1;
+        constexpr int SETS = STATES ? 4 : 1;
+        const int set = STATES ? (warp < 12 ? warp >> 2 : 3) : 0;
         const int j = q >> 1;                  // half
         const int tr = lane & 7, tm = lane >> 3;
         uint32_t off[2];                       // of the loads of value columns 16 hb .. + 16
@@ -333,9 +337,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             const float* w = gates[2 * gs + (ONE ? 0 : j)].w + 2 * (lane & 3);
             const uint32_t xt = sbase + K::OFF_X + xb * K::TILE;
 #pragma unroll 1
-            for (int k = warp >> 2; k < 4; k += SETS) {
-                const int buf = k & 1, use = 2 * c + (k >> 1);
-                const uint32_t col = lane_base + K::COL_WX + 48 * buf;
+            for (int k = set; k < 4; k += SETS) {
+                const int buf = STATES ? k : k & 1, use = STATES ? c : 2 * c + (k >> 1);
+                const uint32_t col = lane_base + (STATES ? K::COL_WX1 : K::COL_WX) + 48 * buf;
                 float2 wv[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) wv[i] = *reinterpret_cast<const float2*>(&w[32 * k + 8 * i]);
@@ -490,6 +494,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         bool on[HEADS];
         float A2[HEADS], bias[HEADS];
         uint16_t raw[HEADS];
+        float run[HEADS];  // first pass: sums of the chunks behind, which are made first
 #pragma unroll
         for (int h = 0; h < HEADS; ++h) {
             const Half f = half_of(p, unit, h);
@@ -497,12 +502,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             A2[h] = on[h] ? -expf(a.A_log[f.head]) * tcf::kLog2e : 0.f;
             bias[h] = on[h] ? a.dt_bias[f.head] : 0.f;
             raw[h] = 0;
+            run[h] = 0.f;
         }
         const uint16_t* dtp = static_cast<const uint16_t*>(a.dt) + (r0 + ln) * a.dts + half_of(p, unit, 0).head;
         auto fetch = [&](int c) {
 #pragma unroll
             for (int h = 0; h < HEADS; ++h)
-                if (on[h] && c * L + ln < rows) raw[h] = dtp[(int64_t)c * L * a.dts + h];
+                if (on[h] && chunk_of(c) * L + ln < rows) raw[h] = dtp[(int64_t)chunk_of(c) * L * a.dts + h];
         };
         auto make_gates = [&](int c) {
             const int gs = c % NGR;
@@ -511,7 +517,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 #pragma unroll
             for (int h = 0; h < HEADS; ++h) {
                 const float v = __uint_as_float((uint32_t)raw[h] << 16) + bias[h];
-                d[h] = on[h] && c * L + ln < rows ? softplus_f32(v) : 0.f;
+                d[h] = on[h] && chunk_of(c) * L + ln < rows ? softplus_f32(v) : 0.f;
                 float g = d[h] * A2[h];
                 g = g < kMinG2 ? kMinG2 : g;  // (written so that a NaN stays one)
                 left[h] = right[h] = g;
@@ -533,6 +539,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                     behind[h] = 0.f;
                     G[h].tot[q] = left[h];
                 }
+                if (STATES) continue;
                 G[h].pre[ln] = left[h];
                 // (the weights of W are rounded to bf16: approximate exponentials do)
                 G[h].prd[ln] = __log2f(d[h]) - left[h];
@@ -543,58 +550,58 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             for (int h = 0; h < HEADS; ++h) {
                 float later = 0.f;
                 for (int b = 3; b > q; --b) later += G[h].tot[b];
-                G[h].w[ln] = d[h] * exp2f(behind[h] + later);
-                if (ln == 0) {
-                    const float all = later + G[h].tot[0];
-                    G[h].lastg = all;
-                    G[h].last = exp2f(all);
+                G[h].w[ln] = d[h] * exp2f(behind[h] + (later + run[h]));
+                if (STATES) {
+                    for (int b = q; b >= 0; --b) later += G[h].tot[b];
+                    run[h] += later;
+                } else if (ln == 0) {
+                    G[h].last = exp2f(later + G[h].tot[0]);
                 }
             }
             arrive(G_FULL + gs);
         };
-        if (nch > 0) {
-            fetch(0);
-            make_gates(0);
-        }
-        if (nch > 1) make_gates(1);
-        float sum_g = 0.f;
-        for (int c = 0; c < nch; ++c) {
-            const int gs = c % NGR;
-            wait(G_FULL + gs, c / NGR);
-            const Gates& G = gates[2 * gs + (ONE ? 0 : j)];
-            const float e = G.last;
-            sum_g += G.lastg;
-            if (c > 0) wait(DS_DONE, c - 1);
-            if (!STATES && c > 0) wait(H_FREE, c - 1);
-            __syncwarp();
-            tc::tc_after_sync();
-#pragma unroll 1
-            for (int n0 = 0; n0 < NP; n0 += 32) {
-                float v[32];
-                tc::tmem_ld32(lane_base + K::COL_S + n0, v);
-                tc::tmem_wait_ld();
-                if constexpr (!STATES)
-                    tc::store_half_row_bf16(sbase + K::OFF_H + (n0 / 64) * K::TILE, ln, (n0 / 32) & 1, v);
-#pragma unroll
-                for (int s = 0; s < 32; s += 8) {
-                    uint32_t u[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        const float2 m = __fmul2_rn(make_float2(v[s + i], v[s + i + 1]), make_float2(e, e));
-                        u[i] = __float_as_uint(m.x);
-                        u[i + 1] = __float_as_uint(m.y);
-                    }
-                    tc::tmem_st8(lane_base + K::COL_S + n0 + s, u);
-                }
-            }
-            tc::tmem_wait_st();
-            tc::fence_async_smem();
+        if (nch > 0) fetch(0);
+        if constexpr (STATES) {
             tc::tc_before_sync();
             arrive(S_READY);
-            if (c + 2 < nch) make_gates(c + 2);
+            for (int c = 0; c < nch; ++c) make_gates(c);
+        } else {
+            for (int c = 0; c < 2 && c < nch; ++c) make_gates(c);
+            for (int c = 0; c < nch; ++c) {
+                const int gs = c % NGR;
+                wait(G_FULL + gs, c / NGR);
+                const float e = gates[2 * gs + (ONE ? 0 : j)].last;
+                if (c > 0) wait(DS_DONE, c - 1);
+                if (c > 0) wait(H_FREE, c - 1);
+                __syncwarp();
+                tc::tc_after_sync();
+#pragma unroll 1
+                for (int n0 = 0; n0 < NP; n0 += 32) {
+                    float v[32];
+                    tc::tmem_ld32(lane_base + K::COL_S + n0, v);
+                    tc::tmem_wait_ld();
+                    tc::store_half_row_bf16(sbase + K::OFF_H + (n0 / 64) * K::TILE, ln, (n0 / 32) & 1, v);
+#pragma unroll
+                    for (int s = 0; s < 32; s += 8) {
+                        uint32_t u[8];
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) {
+                            const float2 m = __fmul2_rn(make_float2(v[s + i], v[s + i + 1]), make_float2(e, e));
+                            u[i] = __float_as_uint(m.x);
+                            u[i + 1] = __float_as_uint(m.y);
+                        }
+                        tc::tmem_st8(lane_base + K::COL_S + n0 + s, u);
+                    }
+                }
+                tc::tmem_wait_st();
+                tc::fence_async_smem();
+                tc::tc_before_sync();
+                arrive(S_READY);
+                if (c + 2 < nch) make_gates(c + 2);
+            }
         }
         // the state that leaves it
-        if (nch > 0) wait(DS_DONE, nch - 1);
+        if (nch > 0) wait(DS_DONE, STATES ? 0 : nch - 1);
         __syncwarp();
         tc::tc_after_sync();
         float* dst = nullptr;
@@ -602,7 +609,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             const int64_t at = (int64_t)(sg.slot + sg.j) * p.units + unit;
             dst = p.part + at * a.N * 128 + ln;
             step = 128;
-            if (pc == 0) p.part_g[at * 2 + j] = sum_g;
+            if (pc == 0) p.part_g[at * 2 + j] = run[ONE ? 0 : j];
         } else if (a.hT && sg.j == sg.n - 1 && live) {
             dst = a.hT + hb;
             step = a.P;
@@ -626,22 +633,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             const Half hf = half_of(p, unit, j);
             const uint32_t ycol = lane_base + K::COL_Y + 64 * j;
             const uint32_t tile = sbase + K::OFF_Z + j * K::TILE;
-            const bool first = (warp & 3) == 0 && lane == 0;
-            // z of chunk c, once the last y has left the tile
-            auto next_z = [&](int c) {
-                tc::bulk_wait_read0();
-                if (a.z && hf.width && !*abort_flag) {
-                    tc::mbar_arrive_expect_tx(&bars[Z_FULL + j], K::TILE);
-                    tma_load_3d(base + K::OFF_Z + j * K::TILE, &p.z, hf.col, hf.head, (int)r0 + c * L, &bars[Z_FULL + j]);
-                } else {
-                    tc::mbar_arrive(&bars[Z_FULL + j]);
-                }
-            };
             for (int c = 0; c < nch; ++c) {
                 const int gs = c % NGR;
                 const int row = (int)r0 + c * L;
-                if (c == 0 && first) next_z(0);
-                __syncwarp();
                 wait(G_FULL + gs, c / NGR);
                 const Gates& G = gates[2 * gs + (ONE ? 0 : j)];
                 float e = G.pre[ln];
@@ -667,8 +661,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 tc::tmem_wait_st();
                 tc::tc_before_sync();
                 arrive(Y_FREE + j);
-                if (c > 0 && first) next_z(c);
-                __syncwarp();
                 wait(Y_FULL + j, 1);
                 wait(Z_FULL + j, c);
                 __syncwarp();
@@ -708,17 +700,34 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 tc::tc_before_sync();
                 arrive(Y_FREE + j);
                 tc::fence_async_smem();
-                tc::named_bar(2 + j, 128);
-                if (first && whole && hf.width && !*abort_flag) {
-                    tma_store_3d(&p.y, tile, hf.col, hf.head, row);
-                    tc::bulk_commit();
+                arrive(Y_OUT + j);
+            }
+        }
+    } else if (warp == 27) {
+        // ======================================================= z and y tiles warp
+        if (!STATES && lane == 0) {
+            const Half hf[2] = {half_of(p, unit, 0), half_of(p, unit, 1)};
+            for (int c = 0; c <= nch; ++c)
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t tile = sbase + K::OFF_Z + j * K::TILE;
+                    if (c > 0) {  // y of the chunk before out of the tile
+                        wait(Y_OUT + j, c - 1);
+                        if (c * L <= rows && hf[j].width && !*abort_flag) {
+                            tma_store_3d(&p.y, tile, hf[j].col, hf[j].head, (int)r0 + (c - 1) * L);
+                            tc::bulk_commit();
+                            tc::bulk_wait_read0();
+                        }
+                    }
+                    if (c == nch) continue;
+                    if (a.z && hf[j].width && !*abort_flag) {
+                        tc::mbar_arrive_expect_tx(&bars[Z_FULL + j], K::TILE);
+                        tma_load_3d(base + K::OFF_Z + j * K::TILE, &p.z, hf[j].col, hf[j].head, (int)r0 + c * L, &bars[Z_FULL + j]);
+                    } else {
+                        tc::mbar_arrive(&bars[Z_FULL + j]);
+                    }
                 }
-                __syncwarp();
-            }
-            if (first) {  // never leave with a copy in flight; y is in global memory
-                tc::bulk_wait0();
-                if (nch > 0) drain(&bars[Z_FULL + j], (uint32_t)(nch - 1) & 1u);
-            }
+            tc::bulk_wait0();  // y is in global memory before the CTA leaves, and no load in flight
+            for (int j = 0; nch > 0 && j < 2; ++j) drain(&bars[Z_FULL + j], (uint32_t)(nch - 1) & 1u);
         }
     } else if (warp == 26) {
         // ============================================================== TMA warp
@@ -728,7 +737,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             if (hf[1].width == 0) hf[1] = hf[0];
             int done = 0;
             for (int c = 0; c < nch && !*abort_flag; ++c) {
-                const int r = (int)(r0 + (int64_t)c * L);
+                const int r = (int)r0 + chunk_of(c) * L;
                 for (int j = 0; j < 2; ++j) {
                     const int xi = 2 * c + j, xb = xi % NXB;
                     if (xi >= NXB) wait(X_DONE + xb, xi / NXB - 1);
@@ -748,8 +757,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                     tma_load_3d(base + K::OFF_B + bc * K::BT + h * K::TILE, &p.b, 64 * h, grp, r, &bars[B_FULL + bc]);
                 if (NBC == 1 && c + 1 < nch)
                     for (int h = 0; h < NH; ++h) {
-                        tma_prefetch_3d(&p.b, 64 * h, grp, r + L);
-                        if (!STATES) tma_prefetch_3d(&p.c, 64 * h, grp, r + L);
+                        tma_prefetch_3d(&p.b, 64 * h, grp, (int)r0 + chunk_of(c + 1) * L);
+                        if (!STATES) tma_prefetch_3d(&p.c, 64 * h, grp, (int)r0 + chunk_of(c + 1) * L);
                     }
                 done = c + 1;
             }
@@ -777,13 +786,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 const uint32_t lb0 = tc::desc_lo(sbase + K::OFF_B + (c % NBC) * K::BT, K::TILE);
                 ready(B_FULL + c % NBC, c / NBC);
                 if (c == nch - 1 && tail < L) ready(CLEAN, 0);
-                ready(S_READY, c);
+                ready(S_READY, STATES ? 0 : c);
                 for (int k = 0; k < 4; ++k) {  // S += (w x)^T B, 32 tokens
-                    const int buf = k & 1;
-                    ready(XQ_FULL + buf, 2 * c + (k >> 1));
+                    const int buf = STATES ? k : k & 1;
+                    ready(XQ_FULL + buf, STATES ? c : 2 * c + (k >> 1));
                     go();
                     if (tc::elect_one()) {
-                        const uint32_t wx = tmem + K::COL_WX + 48 * buf, lb = lb0 + 256 * k;
+                        const uint32_t wx = tmem + (STATES ? K::COL_WX1 : K::COL_WX) + 48 * buf, lb = lb0 + 256 * k;
 #pragma unroll
                         for (int s = 0; s < 3; ++s)
 #pragma unroll
@@ -791,7 +800,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                                 tc::mma_ts<1>(tmem + K::COL_S, wx + 16 * s + 8 * ks, tc::desc(lb + 128 * ks), idS);
                         tc::mma_commit(&bars[XQ_FREE + buf]);
                         if (k == 3) {
-                            tc::mma_commit(&bars[DS_DONE]);
+                            if (!STATES || c == nch - 1) tc::mma_commit(&bars[DS_DONE]);
                             tc::mma_commit(&bars[B_FREE + c % NBC]);
                         }
                     }
@@ -906,11 +915,23 @@ __global__ void __launch_bounds__(256) scan_chain_kernel(const __grid_constant__
     float run = 0.f;
     if (a.h0 && (ln & 63) < hf.width)
         run = a.h0[(((int64_t)seq * a.H + hf.head) * a.N + n) * a.P + hf.col + (ln & 63)];
-    for (int i = 0; i + 1 < s_n; ++i) {
-        const int64_t at = (int64_t)(s_slot + i) * p.units + unit;
-        float* s = p.part + at * a.N * 128 + e;
-        run = fmaf(run, exp2f(p.part_g[at * 2 + (a.P == 128 ? 0 : j)]), *s);
-        *s = run;
+    const int64_t step = (int64_t)p.units * a.N * 128;
+    float* s = p.part + ((int64_t)s_slot * p.units + unit) * a.N * 128 + e;
+    const float* g = p.part_g + ((int64_t)s_slot * p.units + unit) * 2 + (a.P == 128 ? 0 : j);
+    for (int i0 = 0; i0 + 1 < s_n; i0 += 8) {  // eight loads in flight
+        float v[8], d[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i0 + i + 1 < s_n) {
+                v[i] = s[(i0 + i) * step];
+                d[i] = g[(int64_t)(i0 + i) * p.units * 2];
+            }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i0 + i + 1 < s_n) {
+                run = fmaf(run, exp2f(d[i]), v[i]);
+                s[(i0 + i) * step] = run;
+            }
     }
 }
 
@@ -954,7 +975,7 @@ inline ScanPlan plan_scan(int n_seq, int64_t T_total, bool packed, int H, int G,
         // packed sequences end where they like: count a segment more for each
         const int64_t main = (packed ? nseg + n_seq - 1 : n_seq * nseg) * r.units;
         const int64_t first = (packed ? nseg - 1 : n_seq * (nseg - 1)) * r.units;
-        const double cost = (double)((main + sms - 1) / sms) * sc + 0.5 * (double)((first + sms - 1) / sms) * sc +
+        const double cost = (double)((main + sms - 1) / sms) * sc + 0.3 * (double)((first + sms - 1) / sms) * sc +
                             (nseg > 1 ? 4.0 : 0.0);
         if (cut == 1 || cost < best) {
             best = cost;
