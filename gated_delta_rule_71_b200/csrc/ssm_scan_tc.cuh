@@ -80,7 +80,7 @@ struct ScanCfg {
     static constexpr uint32_t OFF_H = OFF_Z + 2 * TILE;
     static constexpr uint32_t OFF_G = OFF_H + BT;       // [NGR][2] Gates
     static constexpr uint32_t OFF_BAR = OFF_G + NGR * 2 * (uint32_t)sizeof(Gates);
-    static constexpr uint32_t SMEM = OFF_BAR + 52 * 8 + 16 + 1024;
+    static constexpr uint32_t SMEM = OFF_BAR + 60 * 8 + 16 + 1024;
     static_assert(SMEM <= 232448, "shared memory budget");
     // tensor memory columns
     static constexpr uint32_t COL_CB = 0;               // fp32 CB, then W of both heads
@@ -92,12 +92,12 @@ struct ScanCfg {
 };
 
 enum : int {
-    B_FULL = 0, B_FREE = B_FULL + 2, C_FULL_ = B_FREE + 2, C_FREE_ = C_FULL_ + 2, X_FULL = C_FREE_ + 2,
+    B_FULL = 0, B_FREE = B_FULL + 4, C_FULL_ = B_FREE + 4, C_FREE_ = C_FULL_ + 2, X_FULL = C_FREE_ + 2,
     X_DONE = X_FULL + 6, Z_FULL = X_DONE + 6, Y_OUT = Z_FULL + 2, G_FULL = Y_OUT + 2, G_FREE = G_FULL + NGR, CB_FULL = G_FREE + NGR, M_FULL, W_FREE,
     XQ_FULL, XQ_FREE = XQ_FULL + 4, S_READY = XQ_FREE + 4, DS_DONE, H_FREE, Y_FULL, Y_FREE = Y_FULL + 2,
     CLEAN = Y_FREE + 2, S_DRAIN, N_SCAN_BARS = S_DRAIN + 2
 };
-static_assert(N_SCAN_BARS <= 52, "barrier slots");
+static_assert(N_SCAN_BARS <= 60, "barrier slots");
 
 // 3-D tiled load of one box (x innermost), completing on `bar`.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
@@ -241,12 +241,13 @@ template <int NP, bool STATES, bool ONE>
 __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_constant__ ScanTcArgs p) {
     using K = ScanCfg<NP>;
     constexpr int NH = K::NH, NXB = K::NXB, NBC = K::NBC;
+    constexpr int NB = STATES ? 2 * NBC : NBC;  // the first pass has no C: its room is for B
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     const uint32_t sbase = (raw_u32 + 1023u) & ~1023u;
     uint8_t* base = smem_raw + (sbase - raw_u32);
     uint64_t* bars = reinterpret_cast<uint64_t*>(base + K::OFF_BAR);
-    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 52);
+    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 60);
     volatile uint32_t* abort_flag = misc + 1;
     Gates* gates = reinterpret_cast<Gates*>(base + K::OFF_G);
     const ScanArgs& a = p.a;
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         for (int i = 0; i < N_SCAN_BARS; ++i) {
             uint32_t n = 1;
             if (i >= X_DONE && i < X_DONE + NXB) n = STATES ? 8 : 3;  // X warps (, the product)
-            if (i == B_FREE || i == B_FREE + 1) n = STATES ? 1 : 2;  // the products of two warps
+            if (i >= B_FREE && i < B_FREE + 4) n = STATES ? 1 : 2;  // the products of two warps
             if (i >= G_FULL && i < G_FULL + NGR) n = 4;
             if (i >= G_FREE && i < G_FREE + NGR) n = STATES ? 16 : 20;
             if (i == M_FULL) n = 8;
@@ -318,14 +319,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 // rows behind the sequence's end belong to another one: x and B to zero
                 // (a zero weight would still carry a NaN through the products)
                 for (int h = 0; h < 2; ++h) wait(X_FULL + (2 * c + h) % NXB, (2 * c + h) / NXB);
-                wait(B_FULL + c % NBC, c / NBC);
+                wait(B_FULL + c % NB, c / NB);
                 if (ln >= tail) {
                     const uint32_t row = (uint32_t)ln * 128u;
                     for (int i = 0; i < 8; ++i) {
                         for (int h = 0; h < 2; ++h)
                             tc::st_shared_v4(sbase + K::OFF_X + ((2 * c + h) % NXB) * K::TILE + row + 16 * i, 0, 0, 0, 0);
                         for (int h = 0; h < NH; ++h)
-                            tc::st_shared_v4(sbase + K::OFF_B + (c % NBC) * K::BT + h * K::TILE + row + 16 * i, 0, 0, 0, 0);
+                            tc::st_shared_v4(sbase + K::OFF_B + (c % NB) * K::BT + h * K::TILE + row + 16 * i, 0, 0, 0, 0);
                     }
                 }
                 tc::fence_async_smem();
@@ -480,12 +481,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             }
         }
 #pragma unroll 1
-        for (int n0 = 0; n0 < NP; n0 += 16) {
-            uint32_t u[16];
+        for (int n0 = 0; n0 < NP; n0 += 32) {
+            uint32_t u[4][8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                u[i] = (src && live && n0 + i < a.N) ? __float_as_uint(src[(int64_t)(n0 + i) * step]) : 0u;
-            tc::tmem_st16(lane_base + K::COL_S + n0, u);
+            for (int i = 0; i < 32; ++i)
+                u[i / 8][i % 8] = (src && live && n0 + i < a.N) ? __float_as_uint(__ldg(&src[(int64_t)(n0 + i) * step])) : 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc::tmem_st8(lane_base + K::COL_S + n0 + 8 * i, u[i]);
         }
         tc::tmem_wait_st();
         // The gates are made here too, two chunks ahead, while the products run: a token a
@@ -669,32 +671,36 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 bf* y = static_cast<bf*>(a.y) + ((int64_t)(row + ln) * a.H + hf.head) * a.P + hf.col;
                 // y takes z's place, each thread in its own row
 #pragma unroll 1
-                for (int n0 = 0; n0 < 64; n0 += 16) {
-                    float v[16];
-                    tc::tmem_ld16(ycol + n0, v);
-                    const uint32_t at[2] = {tile + tc::sw128_off(ln, n0 / 8), tile + tc::sw128_off(ln, n0 / 8 + 1)};
+                for (int n0 = 0; n0 < 64; n0 += 32) {
+                    float v[32];
+                    tc::tmem_ld32(ycol + n0, v);
                     if (a.z) {
-                        const uint4 z0 = tc::ld_shared_v4(at[0]), z1 = tc::ld_shared_v4(at[1]);
-                        const uint32_t zw[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+                        uint4 zu[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) zu[u] = tc::ld_shared_v4(tile + tc::sw128_off(ln, n0 / 8 + u));
                         tc::tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float2 g = conv_silu2(make_float2(bf16_lo(zw[i]), bf16_hi(zw[i])));
-                            v[2 * i] *= g.x;
-                            v[2 * i + 1] *= g.y;
+                        for (int u = 0; u < 4; ++u) {
+                            const uint32_t zw[4] = {zu[u].x, zu[u].y, zu[u].z, zu[u].w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 g = conv_silu2(make_float2(bf16_lo(zw[i]), bf16_hi(zw[i])));
+                                v[8 * u + 2 * i] *= g.x;
+                                v[8 * u + 2 * i + 1] *= g.y;
+                            }
                         }
                     } else {
                         tc::tmem_wait_ld();
                     }
-                    uint32_t ow[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) ow[i] = tc::pack_bf16(v[2 * i], v[2 * i + 1]);
-                    if (whole) {
-                        tc::st_shared_v4(at[0], ow[0], ow[1], ow[2], ow[3]);
-                        tc::st_shared_v4(at[1], ow[4], ow[5], ow[6], ow[7]);
-                    } else if (c * L + ln < rows && n0 < hf.width) {  // rows behind belong to others
-                        *reinterpret_cast<uint4*>(y + n0) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-                        *reinterpret_cast<uint4*>(y + n0 + 8) = make_uint4(ow[4], ow[5], ow[6], ow[7]);
+                    for (int u = 0; u < 4; ++u) {
+                        uint32_t ow[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) ow[i] = tc::pack_bf16(v[8 * u + 2 * i], v[8 * u + 2 * i + 1]);
+                        if (whole)
+                            tc::st_shared_v4(tile + tc::sw128_off(ln, n0 / 8 + u), ow[0], ow[1], ow[2], ow[3]);
+                        else if (c * L + ln < rows && n0 + 8 * u < hf.width)  // rows behind belong to others
+                            *reinterpret_cast<uint4*>(y + n0 + 8 * u) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
                     }
                 }
                 tc::tc_before_sync();
@@ -751,20 +757,21 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                     for (int h = 0; h < NH; ++h)
                         tma_load_3d(base + K::OFF_C + bc * K::BT + h * K::TILE, &p.c, 64 * h, grp, r, &bars[C_FULL_ + bc]);
                 }
-                if (c >= NBC) wait(B_FREE + bc, c / NBC - 1);
-                tc::mbar_arrive_expect_tx(&bars[B_FULL + bc], K::BT);
+                const int bb = c % NB;
+                if (c >= NB) wait(B_FREE + bb, c / NB - 1);
+                tc::mbar_arrive_expect_tx(&bars[B_FULL + bb], K::BT);
                 for (int h = 0; h < NH; ++h)
-                    tma_load_3d(base + K::OFF_B + bc * K::BT + h * K::TILE, &p.b, 64 * h, grp, r, &bars[B_FULL + bc]);
-                if (NBC == 1 && c + 1 < nch)
+                    tma_load_3d(base + K::OFF_B + bb * K::BT + h * K::TILE, &p.b, 64 * h, grp, r, &bars[B_FULL + bb]);
+                if (NB == 1 && c + 1 < nch)
                     for (int h = 0; h < NH; ++h) {
                         tma_prefetch_3d(&p.b, 64 * h, grp, (int)r0 + chunk_of(c + 1) * L);
-                        if (!STATES) tma_prefetch_3d(&p.c, 64 * h, grp, (int)r0 + chunk_of(c + 1) * L);
+                        tma_prefetch_3d(&p.c, 64 * h, grp, (int)r0 + chunk_of(c + 1) * L);
                     }
                 done = c + 1;
             }
             // never leave with a copy in flight
-            for (int c = done >= NBC ? done - NBC : 0; c < done; ++c) {
-                drain(&bars[B_FULL + c % NBC], (c / NBC) & 1);
+            for (int c = done >= NB ? done - NB : 0; c < done; ++c) {
+                drain(&bars[B_FULL + c % NB], (c / NB) & 1);
                 if (!STATES) drain(&bars[C_FULL_ + c % NBC], (c / NBC) & 1);
             }
             for (int i = 2 * done >= NXB ? 2 * done - NXB : 0; i < 2 * done; ++i)
@@ -783,8 +790,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         };
         if (warp == 25) {
             for (int c = 0; c < nch; ++c) {
-                const uint32_t lb0 = tc::desc_lo(sbase + K::OFF_B + (c % NBC) * K::BT, K::TILE);
-                ready(B_FULL + c % NBC, c / NBC);
+                const uint32_t lb0 = tc::desc_lo(sbase + K::OFF_B + (c % NB) * K::BT, K::TILE);
+                ready(B_FULL + c % NB, c / NB);
                 if (c == nch - 1 && tail < L) ready(CLEAN, 0);
                 ready(S_READY, STATES ? 0 : c);
                 for (int k = 0; k < 4; ++k) {  // S += (w x)^T B, 32 tokens
@@ -801,7 +808,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                         tc::mma_commit(&bars[XQ_FREE + buf]);
                         if (k == 3) {
                             if (!STATES || c == nch - 1) tc::mma_commit(&bars[DS_DONE]);
-                            tc::mma_commit(&bars[B_FREE + c % NBC]);
+                            tc::mma_commit(&bars[B_FREE + c % NB]);
                         }
                     }
                     __syncwarp();
