@@ -390,46 +390,41 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 const int gs = c % NGR;
                 const Gates* G = &gates[2 * gs];
                 wait(G_FULL + gs, c / NGR);
-                // row factors of the earlier blocks of 32, while CB is under way
-                float pr[HEADS], rf[HEADS][3];
+                float pr[HEADS], e[HEADS];
 #pragma unroll
-                for (int h = 0; h < HEADS; ++h) {
-                    pr[h] = G[h].pre[ln];
-                    float e = pr[h];
-#pragma unroll
-                    for (int b = 2; b >= 0; --b)
-                        if (b < q) {
-                            rf[h][b] = ex2_approx(e);
-                            e += G[h].tot[b];
-                        }
-                }
+                for (int h = 0; h < HEADS; ++h) e[h] = pr[h] = G[h].pre[ln];
                 wait(CB_FULL, c);
                 __syncwarp();
                 tc::tc_after_sync();
-                // 16 columns of CB become 8 of each head's W
+                // 16 columns of CB become 8 of each head's W: earlier blocks of 32 by factors
+#pragma unroll 1
+                for (int b = q - 1; b >= 0; --b) {
+                    const int kb = 2 * b + kb0;
+                    const uint32_t col = lane_base + K::COL_CB + 16 * kb;
+                    float v[16];
+                    tc::tmem_ld16(col, v);
+                    float2 rf[HEADS];
 #pragma unroll
-                for (int b = 0; b < 3; ++b)
-                    if (b < q) {
-                        const int kb = 2 * b + kb0;
-                        const uint32_t col = lane_base + K::COL_CB + 16 * kb;
-                        float v[16];
-                        tc::tmem_ld16(col, v);
-                        tc::tmem_wait_ld();
-                        uint32_t o[HEADS][8];
-#pragma unroll
-                        for (int s = 0; s < 16; s += 4)
-#pragma unroll
-                            for (int h = 0; h < HEADS; ++h) {
-                                const float4 f = *reinterpret_cast<const float4*>(&G[h].col[16 * kb + s]);
-                                const float2 r2 = make_float2(rf[h][b], rf[h][b]);
-                                const float2 m = __fmul2_rn(make_float2(v[s], v[s + 1]), __fmul2_rn(r2, make_float2(f.x, f.y)));
-                                const float2 n = __fmul2_rn(make_float2(v[s + 2], v[s + 3]), __fmul2_rn(r2, make_float2(f.z, f.w)));
-                                o[h][s / 2] = tc::pack_bf16(m.x, m.y);
-                                o[h][s / 2 + 1] = tc::pack_bf16(n.x, n.y);
-                            }
-#pragma unroll
-                        for (int h = 0; h < HEADS; ++h) tc::tmem_st8(col + 8 * h, o[h]);
+                    for (int h = 0; h < HEADS; ++h) {
+                        const float f = ex2_approx(e[h]);
+                        rf[h] = make_float2(f, f);
+                        e[h] += G[h].tot[b];
                     }
+                    tc::tmem_wait_ld();
+                    uint32_t o[HEADS][8];
+#pragma unroll
+                    for (int s = 0; s < 16; s += 4)
+#pragma unroll
+                        for (int h = 0; h < HEADS; ++h) {
+                            const float4 f = *reinterpret_cast<const float4*>(&G[h].col[16 * kb + s]);
+                            const float2 m = __fmul2_rn(make_float2(v[s], v[s + 1]), __fmul2_rn(rf[h], make_float2(f.x, f.y)));
+                            const float2 n = __fmul2_rn(make_float2(v[s + 2], v[s + 3]), __fmul2_rn(rf[h], make_float2(f.z, f.w)));
+                            o[h][s / 2] = tc::pack_bf16(m.x, m.y);
+                            o[h][s / 2 + 1] = tc::pack_bf16(n.x, n.y);
+                        }
+#pragma unroll
+                    for (int h = 0; h < HEADS; ++h) tc::tmem_st8(col + 8 * h, o[h]);
+                }
                 {  // the block on the diagonal, which is at s == r
                     const int kb = 2 * q + kb0, r = ln - 16 * kb;
                     const uint32_t col = lane_base + K::COL_CB + 16 * kb;
@@ -454,6 +449,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 #pragma unroll
                     for (int h = 0; h < HEADS; ++h) tc::tmem_st8(col + 8 * h, o[h]);
                 }
+#pragma unroll 1
                 for (int b = q + 1; b < 4; ++b)  // above it
                     tc::tmem_st16(lane_base + K::COL_CB + 16 * (2 * b + kb0), zero);
                 tc::tmem_wait_st();
@@ -566,10 +562,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         if constexpr (STATES) {
             tc::tc_before_sync();
             arrive(S_READY);
+#pragma unroll 1
             for (int c = 0; c < nch; ++c) make_gates(c);
         } else {
-            for (int c = 0; c < 2 && c < nch; ++c) make_gates(c);
-            for (int c = 0; c < nch; ++c) {
+#pragma unroll 1
+            for (int c = -2; c < nch; ++c) {
+                if (c + 2 < nch) make_gates(c + 2);
+                if (c < 0) continue;
                 const int gs = c % NGR;
                 wait(G_FULL + gs, c / NGR);
                 const float e = gates[2 * gs + (ONE ? 0 : j)].last;
@@ -578,28 +577,25 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 __syncwarp();
                 tc::tc_after_sync();
 #pragma unroll 1
-                for (int n0 = 0; n0 < NP; n0 += 32) {
-                    float v[32];
-                    tc::tmem_ld32(lane_base + K::COL_S + n0, v);
+                for (int n0 = 0; n0 < NP; n0 += 16) {
+                    float v[16];
+                    uint32_t u[16];
+                    tc::tmem_ld16(lane_base + K::COL_S + n0, v);
                     tc::tmem_wait_ld();
-                    tc::store_half_row_bf16(sbase + K::OFF_H + (n0 / 64) * K::TILE, ln, (n0 / 32) & 1, v);
+                    const uint32_t at = sbase + K::OFF_H + (n0 / 64) * K::TILE;
 #pragma unroll
-                    for (int s = 0; s < 32; s += 8) {
-                        uint32_t u[8];
+                    for (int i = 0; i < 2; ++i)
+                        tc::st_shared_v4(at + tc::sw128_off(ln, (n0 / 8 + i) & 7), tc::pack_bf16(v[8 * i], v[8 * i + 1]),
+                                         tc::pack_bf16(v[8 * i + 2], v[8 * i + 3]), tc::pack_bf16(v[8 * i + 4], v[8 * i + 5]),
+                                         tc::pack_bf16(v[8 * i + 6], v[8 * i + 7]));
 #pragma unroll
-                        for (int i = 0; i < 8; i += 2) {
-                            const float2 m = __fmul2_rn(make_float2(v[s + i], v[s + i + 1]), make_float2(e, e));
-                            u[i] = __float_as_uint(m.x);
-                            u[i + 1] = __float_as_uint(m.y);
-                        }
-                        tc::tmem_st8(lane_base + K::COL_S + n0 + s, u);
-                    }
+                    for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i] * e);
+                    tc::tmem_st16(lane_base + K::COL_S + n0, u);
                 }
                 tc::tmem_wait_st();
                 tc::fence_async_smem();
                 tc::tc_before_sync();
                 arrive(S_READY);
-                if (c + 2 < nch) make_gates(c + 2);
             }
         }
         // the state that leaves it
@@ -630,14 +626,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         // =============================================================== Y warps
         // warpgroup j: half j, one token a thread
         if constexpr (!STATES) {
-            using bf = __nv_bfloat16;
             const int j = (warp >> 2) & 1;
-            const Half hf = half_of(p, unit, j);
             const uint32_t ycol = lane_base + K::COL_Y + 64 * j;
             const uint32_t tile = sbase + K::OFF_Z + j * K::TILE;
             for (int c = 0; c < nch; ++c) {
                 const int gs = c % NGR;
-                const int row = (int)r0 + c * L;
                 wait(G_FULL + gs, c / NGR);
                 const Gates& G = gates[2 * gs + (ONE ? 0 : j)];
                 float e = G.pre[ln];
@@ -667,41 +660,30 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 wait(Z_FULL + j, c);
                 __syncwarp();
                 tc::tc_after_sync();
-                const bool whole = c * L + L <= rows;
-                bf* y = static_cast<bf*>(a.y) + ((int64_t)(row + ln) * a.H + hf.head) * a.P + hf.col;
                 // y takes z's place, each thread in its own row
 #pragma unroll 1
-                for (int n0 = 0; n0 < 64; n0 += 32) {
-                    float v[32];
-                    tc::tmem_ld32(ycol + n0, v);
+                for (int n0 = 0; n0 < 64; n0 += 16) {
+                    float v[16];
+                    tc::tmem_ld16(ycol + n0, v);
+                    const uint32_t at[2] = {tile + tc::sw128_off(ln, n0 / 8), tile + tc::sw128_off(ln, n0 / 8 + 1)};
                     if (a.z) {
-                        uint4 zu[4];
+                        const uint4 z0 = tc::ld_shared_v4(at[0]), z1 = tc::ld_shared_v4(at[1]);
+                        const uint32_t zw[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+                        float2 g[8];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) zu[u] = tc::ld_shared_v4(tile + tc::sw128_off(ln, n0 / 8 + u));
+                        for (int i = 0; i < 8; ++i) g[i] = conv_silu2(make_float2(bf16_lo(zw[i]), bf16_hi(zw[i])));
                         tc::tmem_wait_ld();
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const uint32_t zw[4] = {zu[u].x, zu[u].y, zu[u].z, zu[u].w};
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 g = conv_silu2(make_float2(bf16_lo(zw[i]), bf16_hi(zw[i])));
-                                v[8 * u + 2 * i] *= g.x;
-                                v[8 * u + 2 * i + 1] *= g.y;
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            v[2 * i] *= g[i].x;
+                            v[2 * i + 1] *= g[i].y;
                         }
-                    } else {
-                        tc::tmem_wait_ld();
                     }
+                    tc::tmem_wait_ld();
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        uint32_t ow[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) ow[i] = tc::pack_bf16(v[8 * u + 2 * i], v[8 * u + 2 * i + 1]);
-                        if (whole)
-                            tc::st_shared_v4(tile + tc::sw128_off(ln, n0 / 8 + u), ow[0], ow[1], ow[2], ow[3]);
-                        else if (c * L + ln < rows && n0 + 8 * u < hf.width)  // rows behind belong to others
-                            *reinterpret_cast<uint4*>(y + n0 + 8 * u) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-                    }
+                    for (int u = 0; u < 2; ++u)
+                        tc::st_shared_v4(at[u], tc::pack_bf16(v[8 * u], v[8 * u + 1]), tc::pack_bf16(v[8 * u + 2], v[8 * u + 3]),
+                                         tc::pack_bf16(v[8 * u + 4], v[8 * u + 5]), tc::pack_bf16(v[8 * u + 6], v[8 * u + 7]));
                 }
                 tc::tc_before_sync();
                 arrive(Y_FREE + j);
@@ -711,29 +693,44 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         }
     } else if (warp == 27) {
         // ======================================================= z and y tiles warp
-        if (!STATES && lane == 0) {
-            const Half hf[2] = {half_of(p, unit, 0), half_of(p, unit, 1)};
+        if constexpr (!STATES) {
+#pragma unroll 1
             for (int c = 0; c <= nch; ++c)
+#pragma unroll 1
                 for (int j = 0; j < 2; ++j) {
+                    const Half hf = half_of(p, unit, j);
                     const uint32_t tile = sbase + K::OFF_Z + j * K::TILE;
                     if (c > 0) {  // y of the chunk before out of the tile
                         wait(Y_OUT + j, c - 1);
-                        if (c * L <= rows && hf[j].width && !*abort_flag) {
-                            tma_store_3d(&p.y, tile, hf[j].col, hf[j].head, (int)r0 + (c - 1) * L);
-                            tc::bulk_commit();
-                            tc::bulk_wait_read0();
+                        __syncwarp();
+                        if (hf.width && !*abort_flag) {
+                            if (c * L <= rows) {
+                                if (lane == 0) {
+                                    tma_store_3d(&p.y, tile, hf.col, hf.head, (int)r0 + (c - 1) * L);
+                                    tc::bulk_commit();
+                                    tc::bulk_wait_read0();
+                                }
+                            } else {  // the rows behind the sequence's end belong to another one
+                                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) +
+                                                   ((r0 + (c - 1) * L) * a.H + hf.head) * a.P + hf.col;
+                                for (int i = lane; i < tail * 8; i += 32)
+                                    if (8 * (i & 7) < hf.width)
+                                        *reinterpret_cast<uint4*>(y + (int64_t)(i >> 3) * a.H * a.P + 8 * (i & 7)) =
+                                            tc::ld_shared_v4(tile + tc::sw128_off(i >> 3, i & 7));
+                            }
                         }
                     }
-                    if (c == nch) continue;
-                    if (a.z && hf[j].width && !*abort_flag) {
+                    if (c == nch || lane != 0) continue;
+                    if (a.z && hf.width && !*abort_flag) {
                         tc::mbar_arrive_expect_tx(&bars[Z_FULL + j], K::TILE);
-                        tma_load_3d(base + K::OFF_Z + j * K::TILE, &p.z, hf[j].col, hf[j].head, (int)r0 + c * L, &bars[Z_FULL + j]);
+                        tma_load_3d(base + K::OFF_Z + j * K::TILE, &p.z, hf.col, hf.head, (int)r0 + c * L, &bars[Z_FULL + j]);
                     } else {
                         tc::mbar_arrive(&bars[Z_FULL + j]);
                     }
                 }
-            tc::bulk_wait0();  // y is in global memory before the CTA leaves, and no load in flight
+            if (lane == 0) tc::bulk_wait0();  // y is in global memory before the CTA leaves, no load in flight
             for (int j = 0; nch > 0 && j < 2; ++j) drain(&bars[Z_FULL + j], (uint32_t)(nch - 1) & 1u);
+            __syncwarp();
         }
     } else if (warp == 26) {
         // ============================================================== TMA warp
@@ -794,13 +791,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 ready(B_FULL + c % NB, c / NB);
                 if (c == nch - 1 && tail < L) ready(CLEAN, 0);
                 ready(S_READY, STATES ? 0 : c);
+#pragma unroll 1
                 for (int k = 0; k < 4; ++k) {  // S += (w x)^T B, 32 tokens
                     const int buf = STATES ? k : k & 1;
                     ready(XQ_FULL + buf, STATES ? c : 2 * c + (k >> 1));
                     go();
                     if (tc::elect_one()) {
                         const uint32_t wx = tmem + (STATES ? K::COL_WX1 : K::COL_WX) + 48 * buf, lb = lb0 + 256 * k;
-#pragma unroll
+#pragma unroll 1
                         for (int s = 0; s < 3; ++s)
 #pragma unroll
                             for (int ks = 0; ks < 2; ++ks)
@@ -825,11 +823,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 if (c > 0) ready(W_FREE, c - 1);  // the last chunk's W has been read
                 go();
                 if (tc::elect_one()) {
-                    tc::mma_ss<0>(tmem + K::COL_CB, tc::desc(lc), tc::desc(lbk), idCB);
-#pragma unroll
-                    for (int k = 1; k < NP / 16; ++k) {
+#pragma unroll 1
+                    for (int k = 0; k < NP / 16; ++k) {
                         const uint32_t o = (k >> 2) * (K::TILE / 16) + (k & 3) * 2;
-                        tc::mma_ss<1>(tmem + K::COL_CB, tc::desc(lc + o), tc::desc(lbk + o), idCB);
+                        tc::mma_bf16(tmem + K::COL_CB, tc::desc(lc + o), tc::desc(lbk + o), idCB, k > 0);
                     }
                     tc::mma_commit(&bars[CB_FULL]);
                     tc::mma_commit(&bars[B_FREE + bc]);
@@ -843,11 +840,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 go();
                 if (tc::elect_one()) {  // C h, both halves
                     const uint32_t lh = tc::desc_lo(sbase + K::OFF_H, 16);
-                    tc::mma_ss<0>(tmem + K::COL_Y, tc::desc(lc), tc::desc(lh), idCB);
-#pragma unroll
-                    for (int k = 1; k < NP / 16; ++k) {
+#pragma unroll 1
+                    for (int k = 0; k < NP / 16; ++k) {
                         const uint32_t o = (k >> 2) * (K::TILE / 16) + (k & 3) * 2;
-                        tc::mma_ss<1>(tmem + K::COL_Y, tc::desc(lc + o), tc::desc(lh + o), idCB);
+                        tc::mma_bf16(tmem + K::COL_Y, tc::desc(lc + o), tc::desc(lh + o), idCB, k > 0);
                     }
                     tc::mma_commit(&bars[Y_FULL]);
                     tc::mma_commit(&bars[Y_FULL + 1]);
@@ -865,7 +861,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                     if (tc::elect_one()) {
                         const uint32_t lx = tc::desc_lo(sbase + K::OFF_X + xb * K::TILE, K::TILE);
                         const uint32_t w = tmem + K::COL_CB + (ONE ? 0 : 8 * j), d = tmem + K::COL_Y + 64 * j;
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < 8; ++k) tc::mma_ts<1>(d, w + 16 * k, tc::desc(lx + 128 * k), idY1);
                         tc::mma_commit(&bars[Y_FULL + j]);
                         tc::mma_commit(&bars[X_DONE + xb]);
@@ -963,27 +959,39 @@ struct ScanPlan {
     int64_t slots;    // segment states: full segments that are not a sequence's last, at most
 };
 
-// How long the segments are.  One segment a sequence keeps the SMs busy when there
-// are many (sequence, unit) chains.  With fewer, cutting a sequence costs a first
-// pass over its products into the state (about half a chunk's time) for every
-// segment but the last, and shortens the walk: the cheapest of the cuts into whole
-// waves, in chunk times.
+// How long the segments are: the cheapest cut, in times of one chunk of the main pass (3 us).
+// A CTA costs its chunks and about 2 more to start and end; a chunk of the first pass
+// costs 0.3 and a CTA of it 1.5; the two more launches 3.  One segment a sequence is the
+// plan when there are sequences and units enough for the SMs; a lone long sequence is cut
+// into as many segments as fill them.  Packed lengths are not known here: the longest of
+// n is taken as the mean of the longest of n random parts, and the segments as balanced
+// by the order of the blocks.
 inline ScanPlan plan_scan(int n_seq, int64_t T_total, bool packed, int H, int G, int P, int sms) {
     ScanPlan r;
     r.pairs = P == 128 ? H / G : (H / G + 1) / 2;
     r.units = G * r.pairs;
     const int64_t len = packed ? T_total : T_total / n_seq;
     const int64_t chunks = (len + L - 1) / L;
+    double share = 0;  // of the longest packed sequence
+    for (int i = 1; i <= n_seq && i <= 64; ++i) share += 1.0 / i / n_seq;
+    const double longest = packed && n_seq > 1 ? chunks * (share < 1 ? share : 1) : (double)chunks;
     double best = 0;
     r.seg_chunks = 0x400000;
     for (int cut = 1; cut <= 160 && (cut == 1 || cut * 4 <= chunks); ++cut) {
         const int64_t sc = (chunks + cut - 1) / cut;
         const int64_t nseg = chunks ? (chunks + sc - 1) / sc : 1;
-        // packed sequences end where they like: count a segment more for each
-        const int64_t main = (packed ? nseg + n_seq - 1 : n_seq * nseg) * r.units;
-        const int64_t first = (packed ? nseg - 1 : n_seq * (nseg - 1)) * r.units;
-        const double cost = (double)((main + sms - 1) / sms) * sc + 0.3 * (double)((first + sms - 1) / sms) * sc +
-                            (nseg > 1 ? 4.0 : 0.0);
+        double cost;
+        if (packed) {
+            const double u = (double)r.units / sms, part = longest > sc ? 1.0 - (double)sc / (2 * longest) : 0.0;
+            const double tail = sc < longest ? (double)sc : longest;
+            cost = u * chunks + 0.5 * tail + 2.0 * u * (nseg + n_seq);
+            if (cost < tail) cost = tail;
+            if (cut > 1) cost += part * (0.3 * u * chunks + 1.5 * u * nseg) + 3.0;
+        } else {
+            const int64_t main = n_seq * nseg * r.units, first = n_seq * (nseg - 1) * r.units;
+            cost = (double)((main + sms - 1) / sms) * (sc + 2);
+            if (nseg > 1) cost += (double)((first + sms - 1) / sms) * (0.3 * sc + 1.5) + 3.0;
+        }
         if (cut == 1 || cost < best) {
             best = cost;
             r.seg_chunks = (int)(sc > 0 ? sc : 1);
