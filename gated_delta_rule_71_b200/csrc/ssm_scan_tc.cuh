@@ -59,6 +59,7 @@ struct ScanTcArgs {
     ScanArgs a;
     int pairs;                  // CTAs' worth of value lanes of a group
     int units;                  // of all groups
+    int per;                    // heads of a group
     int seg_chunks;             // chunks of a segment
     float* part;                // [slots, units, N, 128] segment states
     float* part_g;              // [slots, units, 2] segment sums of g (log2)
@@ -187,7 +188,7 @@ __device__ __forceinline__ int64_t seq_segments(int64_t len, int64_t seg) {
 // segments only.  Called by one whole warp; false when there is no segment k.
 struct Segment { int seq; int j; int n; int slot; };
 template <bool STATES>
-__device__ inline bool find_segment(const ScanArgs& a, int64_t k, int64_t seg, int lane, Segment& o) {
+__device__ __noinline__ bool find_segment(const ScanArgs& a, int64_t k, int64_t seg, int lane, Segment& o) {
     if (!a.cu) {
         const int64_t n = seq_segments(a.T, seg), per = STATES ? n - 1 : n;
         if (per == 0 || k >= per * a.n_seq) return false;
@@ -230,10 +231,10 @@ __device__ inline bool find_segment(const ScanArgs& a, int64_t k, int64_t seg, i
 // The value lanes of a unit: half j is 64 lanes of one head.
 struct Half { int head; int col; int width; };  // width 0: no such head
 __device__ __forceinline__ Half half_of(const ScanTcArgs& p, int unit, int j) {
-    const int per = p.a.H / p.a.G, g = unit / p.pairs, u = unit - g * p.pairs;
-    if (p.a.P == 128) return Half{g * per + u, 64 * j, 64};
+    const int g = unit / p.pairs, u = unit - g * p.pairs;
+    if (p.a.P == 128) return Half{g * p.per + u, 64 * j, 64};
     const int h = 2 * u + j;
-    return Half{g * per + h, 0, h < per ? p.a.P : 0};
+    return Half{g * p.per + h, 0, h < p.per ? p.a.P : 0};
 }
 
 // Grid: segments * units.  ONE: the 128 lanes are one head (P = 128).
@@ -265,6 +266,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     const int nch = (int)__reduce_max_sync(0xffffffffu, (uint32_t)((rows + L - 1) / L));
     const int tail = rows - (nch - 1) * L;  // rows of the last chunk
     const int grp = unit / p.pairs;
+    // the two halves (as half_of, without its division)
+    auto half = [&](int j) {
+        const int u = unit - grp * p.pairs, h = 2 * u + j;
+        return ONE ? Half{grp * p.per + u, 64 * j, 64} : Half{grp * p.per + h, 0, h < p.per ? a.P : 0};
+    };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < N_SCAN_BARS; ++i) {
@@ -322,6 +328,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 wait(B_FULL + c % NB, c / NB);
                 if (ln >= tail) {
                     const uint32_t row = (uint32_t)ln * 128u;
+#pragma unroll 1
                     for (int i = 0; i < 8; ++i) {
                         for (int h = 0; h < 2; ++h)
                             tc::st_shared_v4(sbase + K::OFF_X + ((2 * c + h) % NXB) * K::TILE + row + 16 * i, 0, 0, 0, 0);
@@ -383,7 +390,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             float Dh[HEADS];
 #pragma unroll
             for (int h = 0; h < HEADS; ++h) {
-                const Half hf = half_of(p, unit, h);
+                const Half hf = half(h);
                 Dh[h] = a.D && hf.width ? a.D[hf.head] : 0.f;
             }
             for (int c = 0; c < nch; ++c) {
@@ -461,13 +468,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     } else if (warp < 16) {
         // =============================================================== S warps
         const int j = ln >> 6, pc = ln & 63;
-        const Half hf = half_of(p, unit, j);
+        const Half hf = half(j);
         const bool live = pc < hf.width;
         const int64_t hb = (((int64_t)sg.seq * a.H + hf.head) * a.N) * a.P + hf.col + pc;
         // the state that enters the segment
         const float* src = nullptr;
         int64_t step = 0;
-        if (!STATES) {
+        if (!STATES && live) {
             if (sg.j > 0) {
                 src = p.part + ((int64_t)(sg.slot + sg.j - 1) * p.units + unit) * a.N * 128 + ln;
                 step = 128;
@@ -477,13 +484,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             }
         }
 #pragma unroll 1
-        for (int n0 = 0; n0 < NP; n0 += 32) {
-            uint32_t u[4][8];
+        for (int n0 = 0; n0 < NP; n0 += 16) {
+            uint32_t u[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                u[i / 8][i % 8] = (src && live && n0 + i < a.N) ? __float_as_uint(__ldg(&src[(int64_t)(n0 + i) * step])) : 0u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tc::tmem_st8(lane_base + K::COL_S + n0 + 8 * i, u[i]);
+            for (int i = 0; i < 16; ++i) {
+                u[i] = src && n0 + i < a.N ? __float_as_uint(__ldg(src)) : 0u;
+                src += step;
+            }
+            tc::tmem_st16(lane_base + K::COL_S + n0, u);
         }
         tc::tmem_wait_st();
         // The gates are made here too, two chunks ahead, while the products run: a token a
@@ -495,14 +503,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         float run[HEADS];  // first pass: sums of the chunks behind, which are made first
 #pragma unroll
         for (int h = 0; h < HEADS; ++h) {
-            const Half f = half_of(p, unit, h);
+            const Half f = half(h);
             on[h] = f.width > 0;
             A2[h] = on[h] ? -expf(a.A_log[f.head]) * tcf::kLog2e : 0.f;
             bias[h] = on[h] ? a.dt_bias[f.head] : 0.f;
             raw[h] = 0;
             run[h] = 0.f;
         }
-        const uint16_t* dtp = static_cast<const uint16_t*>(a.dt) + (r0 + ln) * a.dts + half_of(p, unit, 0).head;
+        const uint16_t* dtp = static_cast<const uint16_t*>(a.dt) + (r0 + ln) * a.dts + half(0).head;
         auto fetch = [&](int c) {
 #pragma unroll
             for (int h = 0; h < HEADS; ++h)
@@ -613,14 +621,16 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             step = a.P;
         }
 #pragma unroll 1
-        for (int n0 = 0; n0 < NP; n0 += 32) {
-            float v[32];
-            tc::tmem_ld32(lane_base + K::COL_S + n0, v);
+        for (int n0 = 0; n0 < NP; n0 += 16) {
+            float v[16];
+            tc::tmem_ld16(lane_base + K::COL_S + n0, v);
             tc::tmem_wait_ld();
             if (dst)
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (n0 + i < a.N) dst[(int64_t)(n0 + i) * step] = v[i];
+                for (int i = 0; i < 16; ++i) {
+                    if (n0 + i < a.N) *dst = v[i];
+                    dst += step;
+                }
         }
     } else if (warp < 24) {
         // =============================================================== Y warps
@@ -698,7 +708,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             for (int c = 0; c <= nch; ++c)
 #pragma unroll 1
                 for (int j = 0; j < 2; ++j) {
-                    const Half hf = half_of(p, unit, j);
+                    const Half hf = half(j);
                     const uint32_t tile = sbase + K::OFF_Z + j * K::TILE;
                     if (c > 0) {  // y of the chunk before out of the tile
                         wait(Y_OUT + j, c - 1);
@@ -713,6 +723,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                             } else {  // the rows behind the sequence's end belong to another one
                                 __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) +
                                                    ((r0 + (c - 1) * L) * a.H + hf.head) * a.P + hf.col;
+#pragma unroll 1
                                 for (int i = lane; i < tail * 8; i += 32)
                                     if (8 * (i & 7) < hf.width)
                                         *reinterpret_cast<uint4*>(y + (int64_t)(i >> 3) * a.H * a.P + 8 * (i & 7)) =
@@ -729,16 +740,18 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                     }
                 }
             if (lane == 0) tc::bulk_wait0();  // y is in global memory before the CTA leaves, no load in flight
+#pragma unroll 1
             for (int j = 0; nch > 0 && j < 2; ++j) drain(&bars[Z_FULL + j], (uint32_t)(nch - 1) & 1u);
             __syncwarp();
         }
     } else if (warp == 26) {
         // ============================================================== TMA warp
         if (lane == 0) {
-            Half hf[2] = {half_of(p, unit, 0), half_of(p, unit, 1)};
+            Half hf[2] = {half(0), half(1)};
             // a missing second head reads the first one's columns: nothing uses them
             if (hf[1].width == 0) hf[1] = hf[0];
             int done = 0;
+#pragma unroll 1
             for (int c = 0; c < nch && !*abort_flag; ++c) {
                 const int r = (int)r0 + chunk_of(c) * L;
                 for (int j = 0; j < 2; ++j) {
@@ -767,10 +780,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 done = c + 1;
             }
             // never leave with a copy in flight
+#pragma unroll 1
             for (int c = done >= NB ? done - NB : 0; c < done; ++c) {
                 drain(&bars[B_FULL + c % NB], (c / NB) & 1);
                 if (!STATES) drain(&bars[C_FULL_ + c % NBC], (c / NBC) & 1);
             }
+#pragma unroll 1
             for (int i = 2 * done >= NXB ? 2 * done - NXB : 0; i < 2 * done; ++i)
                 drain(&bars[X_FULL + i % NXB], (i / NXB) & 1);
         }
@@ -1047,6 +1062,7 @@ inline cudaError_t launch_scan_tc(const ScanArgs& a, int64_t rows, const ScanPla
     p.a = a;
     p.pairs = r.pairs;
     p.units = r.units;
+    p.per = a.H / a.G;
     p.seg_chunks = r.seg_chunks;
     p.part = static_cast<float*>(workspace);
     p.part_g = p.part + r.slots * r.units * a.N * 128;
