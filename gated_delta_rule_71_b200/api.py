@@ -6,7 +6,7 @@ dtypes and devices, allocates outputs with torch, and forwards raw pointers.
 """
 from __future__ import annotations
 
-import contextlib
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -421,9 +421,20 @@ def conv1d_update(x: torch.Tensor, w: torch.Tensor, conv_state: torch.Tensor,
     return y
 
 
-def _on(dev: torch.device):
-    """The operands' device made current for a launch, where it is not already."""
-    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+# The current stream as an integer without building a Stream object (2 us of a call), where
+# this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch(dev: torch.device, name: str, *args) -> None:
+    """A library call on dev's current stream, with dev made current where it is not already."""
+    index = dev.index
+    stream = _raw_stream(index) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    if index == torch.cuda.current_device():
+        _lib.call(name, *args, stream)
+    else:
+        with torch.cuda.device(dev):
+            _lib.call(name, *args, stream)
 
 
 def _row_stride(t: torch.Tensor, name: str, inner: int) -> int:
@@ -448,6 +459,7 @@ def _row_stride(t: torch.Tensor, name: str, inner: int) -> int:
     return st
 
 
+@functools.lru_cache(maxsize=256)
 def ssm_scan_workspace_size(n_seq: int, T_total: int, H: int, G: int, P: int, N: int,
                             dtype=torch.bfloat16) -> int:
     return int(_lib.load().gdn_ssm_scan_workspace_size(n_seq, T_total, H, G, P, N, _DT[dtype]))
@@ -478,12 +490,12 @@ def ssm_scan(x: torch.Tensor, dt: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tens
                         (z, "z", (B, T, H, P))):
         if t is not None or n != "z":
             _need(t, n, x.dtype, dev, contiguous=False)
-            if tuple(t.shape) != shape:
+            if t.shape != shape:
                 raise ValueError(f"{n} must be {list(shape)}")
     for t, n in ((A_log, "A_log"), (dt_bias, "dt_bias"), (D, "D")):
         if t is not None or n != "D":
             _need(t, n, torch.float32, dev)
-            if tuple(t.shape) != (H,):
+            if t.shape != (H,):
                 raise ValueError(f"{n} must be [H]")
     n_seq = B
     if cu_seqlens is not None:
@@ -493,12 +505,12 @@ def ssm_scan(x: torch.Tensor, dt: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tens
         n_seq = cu_seqlens.numel() - 1
     if h0 is not None:
         _need(h0, "h0", torch.float32, dev)
-        if tuple(h0.shape) != (n_seq, H, N, P):
+        if h0.shape != (n_seq, H, N, P):
             raise ValueError("h0 must be [n_seq, H, N, P]")
     if out is None:
-        out = torch.empty((B, T, H, P), dtype=x.dtype, device=dev)
+        out = x.new_empty((B, T, H, P))
     _need(out, "out", x.dtype, dev)
-    if tuple(out.shape) != (B, T, H, P):
+    if out.shape != (B, T, H, P):
         raise ValueError("out must be [B, T, H, P]")
     hT = torch.empty((n_seq, H, N, P), dtype=torch.float32, device=dev) if output_final_state else None
     need = ssm_scan_workspace_size(n_seq, B * T, H, G, P, N, x.dtype)
@@ -506,17 +518,16 @@ def ssm_scan(x: torch.Tensor, dt: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tens
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is not None:
         _need(workspace, "workspace", None, dev)
-    with _on(dev):
-        _lib.call("gdn_ssm_scan", _ptr(x), _row_stride(x, "x", 2), _ptr(dt), _row_stride(dt, "dt", 1),
-                  _ptr(Bm), _row_stride(Bm, "Bm", 2), _ptr(Cm), _row_stride(Cm, "Cm", 2), _ptr(z),
-                  0 if z is None else _row_stride(z, "z", 2), _DT[x.dtype], _ptr(A_log),
-                  _ptr(dt_bias), _ptr(D), _ptr(h0), _ptr(cu_seqlens), n_seq, B, T, H, G, P, N,
-                  _ptr(out), _ptr(hT), _ptr(workspace),
-                  0 if workspace is None else workspace.numel() * workspace.element_size(),
-                  _stream(x))
+    _launch(dev, "gdn_ssm_scan", x.data_ptr(), _row_stride(x, "x", 2), dt.data_ptr(),
+            _row_stride(dt, "dt", 1), Bm.data_ptr(), _row_stride(Bm, "Bm", 2), Cm.data_ptr(),
+            _row_stride(Cm, "Cm", 2), _ptr(z), 0 if z is None else _row_stride(z, "z", 2),
+            _DT[x.dtype], A_log.data_ptr(), dt_bias.data_ptr(), _ptr(D), _ptr(h0), _ptr(cu_seqlens),
+            n_seq, B, T, H, G, P, N, out.data_ptr(), _ptr(hT), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size())
     return out, hT
 
 
+@functools.lru_cache(maxsize=256)
 def ssm_decode_step_workspace_size(n: int, H: int, G: int, P: int, N: int) -> int:
     return int(_lib.load().gdn_ssm_decode_step_workspace_size(n, H, G, P, N))
 
@@ -547,7 +558,7 @@ def ssm_decode_step(row: torch.Tensor, dt: torch.Tensor, conv_w: torch.Tensor,
             strides.append(0)
             continue
         _need(t, nm, torch.bfloat16, dev, contiguous=False)
-        if tuple(t.shape) != (n, width):
+        if t.shape != (n, width):
             raise ValueError(f"{nm} must be [n, {width}]")
         if width > 1 and t.stride(1) != 1:
             raise ValueError(f"{nm} needs a contiguous last dimension")
@@ -558,40 +569,39 @@ def ssm_decode_step(row: torch.Tensor, dt: torch.Tensor, conv_w: torch.Tensor,
     W = conv_w.shape[1]
     _need(conv_state, "conv_state", torch.bfloat16, dev)
     _need(state, "state", torch.float32, dev)
-    if state.dim() != 4 or tuple(state.shape[1:]) != (H, N, P):
+    if state.dim() != 4 or state.shape[1:] != (H, N, P):
         raise ValueError("state must be [n_slots, H, N, P]")
     n_slots = state.shape[0]
-    if conv_state.dim() != 3 or tuple(conv_state.shape) != (n_slots, C, W - 1):
+    if conv_state.dim() != 3 or conv_state.shape != (n_slots, C, W - 1):
         raise ValueError("conv_state must be [n_slots, C, W-1]")
     for t, nm, size in ((A_log, "A_log", H), (dt_bias, "dt_bias", H), (D, "D", H),
                         (conv_bias, "conv_bias", C)):
         if t is None and nm in ("D", "conv_bias"):
             continue
         _need(t, nm, torch.float32, dev)
-        if tuple(t.shape) != (size,):
+        if t.shape != (size,):
             raise ValueError(f"{nm} must be [{size}]")
     if state_indices is None:
         if n_slots < n:
             raise ValueError("without state_indices, state must have at least n slots")
     else:
         _need(state_indices, "state_indices", torch.int32, dev)
-        if tuple(state_indices.shape) != (n,):
+        if state_indices.shape != (n,):
             raise ValueError("state_indices must be int32 [n]")
     if out is None:
-        out = torch.empty((n, H, P), dtype=torch.bfloat16, device=dev)
+        out = row.new_empty((n, H, P))
     _need(out, "out", torch.bfloat16, dev)
-    if tuple(out.shape) != (n, H, P):
+    if out.shape != (n, H, P):
         raise ValueError("out must be [n, H, P]")
     if workspace is None:
         workspace = torch.empty(max(ssm_decode_step_workspace_size(n, H, G, P, N), 1),
                                 dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", None, dev)
-    with _on(dev):
-        _lib.call("gdn_ssm_decode_step", _ptr(row), strides[0], _ptr(dt), strides[1], _ptr(z),
-                  strides[2], _ptr(conv_w), _ptr(conv_bias), W, _ptr(conv_state),
-                  int(bool(activation)), _ptr(A_log), _ptr(dt_bias), _ptr(D), n, H, G, P, N,
-                  _ptr(state), _ptr(state_indices), n_slots, _ptr(out), _ptr(workspace),
-                  workspace.numel() * workspace.element_size(), _stream(row))
+    _launch(dev, "gdn_ssm_decode_step", row.data_ptr(), strides[0], dt.data_ptr(), strides[1], _ptr(z),
+            strides[2], conv_w.data_ptr(), _ptr(conv_bias), W, conv_state.data_ptr(),
+            int(bool(activation)), A_log.data_ptr(), dt_bias.data_ptr(), _ptr(D), n, H, G, P, N,
+            state.data_ptr(), _ptr(state_indices), n_slots, out.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
     return out
 
 
@@ -612,7 +622,7 @@ def rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
     D = x.shape[-1]
     rows = x.numel() // D
     _need(weight, "weight", torch.float32, dev)
-    if tuple(weight.shape) != (D,):
+    if weight.shape != (D,):
         raise ValueError("weight must be [D]")
     strides = []
     for t, n in ((x, "x"), (residual, "residual")):
@@ -626,16 +636,16 @@ def rmsnorm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
             raise ValueError(f"{n} rows must be contiguous and must not overlap")
         strides.append(t.stride(0) if t.dim() == 2 and rows > 1 else D)
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+        out = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
+    blocks = (*x.shape[:-1], -(-D // 128))
     if scales is None:
-        scales = torch.empty((*x.shape[:-1], -(-D // 128)), dtype=torch.float32, device=dev)
+        scales = weight.new_empty(blocks)
     _need(out, "out", torch.float8_e4m3fn, dev)
     _need(scales, "scales", torch.float32, dev)
-    if out.shape != x.shape or tuple(scales.shape) != (*x.shape[:-1], -(-D // 128)):
+    if out.shape != x.shape or scales.shape != blocks:
         raise ValueError("out must have x's shape and scales [..., ceil(D/128)]")
-    with _on(dev):
-        _lib.call("gdn_rmsnorm_fp8", _ptr(x), strides[0], _ptr(residual), strides[1], _DT[x.dtype],
-                  _ptr(weight), float(eps), rows, D, _ptr(out), _ptr(scales), _stream(x))
+    _launch(dev, "gdn_rmsnorm_fp8", x.data_ptr(), strides[0], _ptr(residual), strides[1],
+            _DT[x.dtype], weight.data_ptr(), eps, rows, D, out.data_ptr(), scales.data_ptr())
     return out, scales
 
 
@@ -659,9 +669,9 @@ def fp8_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scale
     kb = -(-K // 128)
     _need(a_scales, "a_scales", torch.float32, dev)
     _need(w_scales, "w_scales", torch.float32, dev)
-    if tuple(a_scales.shape) != (*a.shape[:-1], kb):
+    if a_scales.shape != (*a.shape[:-1], kb):
         raise ValueError("a_scales must be [..., ceil(K/128)]")
-    if tuple(w_scales.shape) != (-(-N // 128), kb):
+    if w_scales.shape != (-(-N // 128), kb):
         raise ValueError("w_scales must be [ceil(N/128), ceil(K/128)]")
     strides = []
     for t, n, rows in ((a, "a", M), (w, "w", N)):
@@ -669,11 +679,11 @@ def fp8_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scale
             raise ValueError(f"{n} rows must be contiguous and must not overlap")
         strides.append(t.stride(0) if t.dim() == 2 and rows > 1 else K)
     if out is None:
-        out = torch.empty((*a.shape[:-1], N), dtype=out_dtype, device=dev)
-    _need(out, "out", out_dtype, dev)
-    if tuple(out.shape) != (*a.shape[:-1], N):
-        raise ValueError("out must be [..., N]")
-    with _on(dev):
-        _lib.call("gdn_fp8_matmul", _ptr(a), strides[0], _ptr(a_scales), _ptr(w), strides[1],
-                  _ptr(w_scales), M, N, K, _ptr(out), _DT[out_dtype], _stream(a))
+        out = a_scales.new_empty((*a.shape[:-1], N), dtype=out_dtype)
+    else:
+        _need(out, "out", out_dtype, dev)
+        if out.shape != (*a.shape[:-1], N):
+            raise ValueError("out must be [..., N]")
+    _launch(dev, "gdn_fp8_matmul", a.data_ptr(), strides[0], a_scales.data_ptr(), w.data_ptr(),
+            strides[1], w_scales.data_ptr(), M, N, K, out.data_ptr(), _DT[out_dtype])
     return out

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -40,9 +41,13 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 int num_sms() {
+    static std::atomic<int> known[64];  // by device; 0: not asked yet
     int dev = 0, n = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess)
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (cudaGetDevice(&dev) != cudaSuccess) return n;
+    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    n = 148;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && dev >= 0 && dev < 64)
+        known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -719,15 +724,15 @@ gdn_status gdn_ssm_scan(const void* x, int64_t x_stride, const void* dt, int64_t
                           (const void*)h0, (const void*)cu_seqlens, (const void*)hT})
         if (p && !aligned_to(p, 4)) return GDN_ERR_INVALID_ARG;
     if (hT && hT == h0) return GDN_ERR_INVALID_ARG;
-    const size_t need = gdn_ssm_scan_workspace_size(n_seq, rows, H, G, P, N, dtype);
+    const gdn::ssm::ScanPlan r =
+        gdn::ssm::plan_scan(n_seq, rows, cu_seqlens != nullptr, H, G, P, num_sms());
+    const size_t need = dtype == GDN_BF16 ? gdn::ssm::scan_part_bytes(r, N) : 0;
     if (need && (!workspace || ws_bytes < need || !aligned16(workspace))) return GDN_ERR_INVALID_ARG;
     gdn::ssm::ScanArgs a{x,    Bm,      Cm, dt, z,  x_stride,   b_stride, c_stride, dt_stride,
                          z_stride, A_log, dt_bias, D, h0, cu_seqlens, n_seq, T, H, G, P, N, y, hT};
     cudaStream_t st = as_stream(stream);
     if (dtype == GDN_F32) return launch_scan_simt<float>(a, st);
     using gdn::ssm::tma_rows;
-    const gdn::ssm::ScanPlan r =
-        gdn::ssm::plan_scan(n_seq, rows, cu_seqlens != nullptr, H, G, P, num_sms());
     // rows on 16 bytes (y is [rows, H, P] and needs the same) take the tensor cores
     if (rows > 0 && rows < ((int64_t)1 << 31) && tma_rows(x, x_stride) && tma_rows(Bm, b_stride) &&
         tma_rows(Cm, c_stride) && (!z || tma_rows(z, z_stride)) && aligned16(y) && r.segments * r.units < 0x7fffffff &&
