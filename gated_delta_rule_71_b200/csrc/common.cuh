@@ -78,4 +78,33 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t phase, uint32_
     return false;
 }
 
+// One poll that may sleep up to `ns` nanoseconds in hardware: in kernels where most warps
+// wait most of the time, short polls take the issue slots and the shared-memory pipe from
+// the ones that work (the state space scan lost a quarter of its time to them).
+__device__ __forceinline__ bool try_wait_ns(uint32_t bar, uint32_t phase, uint32_t ns) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(phase), "r"(ns)
+        : "memory");
+    return ok != 0;
+}
+constexpr uint32_t kNap = 20000, kNaps = 1u << 17;  // 20 us a poll, a few seconds in all
+// Bounded wait of napping polls that honours the CTA's abort flag, and raises it when it
+// gives up.
+__device__ __forceinline__ void nap_wait(uint64_t* bar, uint32_t phase, volatile uint32_t* abort) {
+    const uint32_t at = smem_u32(bar);
+    uint32_t i = 0;
+#pragma unroll 1
+    while (!try_wait_ns(at, phase, kNap)) {
+        if (*abort || ++i >= kNaps) {
+            *abort = 1u;
+            break;
+        }
+    }
+}
+
 }  // namespace gdn

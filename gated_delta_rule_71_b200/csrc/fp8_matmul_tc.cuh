@@ -29,11 +29,12 @@ constexpr uint32_t kLaneTile = 128 * 128;  // bytes of one 128-row tile of a K b
 
 template <bool TOKENS, int TN>
 struct Cfg {
-    static constexpr int NPW = TN >= 128 ? 8 : 4;         // promotion warps
+    static constexpr int NPW = TN >= 64 ? TN / 16 : 4;    // promotion warps: 64 columns a thread at most
     static constexpr int CPT = TN / (NPW / 4);            // columns of one promotion thread
     static constexpr int THREADS = 32 * (NPW + 2);
     static constexpr uint32_t STAGE = kLaneTile + TN * 128;
-    static constexpr int NS = TN == 256 ? 4 : 6;          // ring stages
+    static constexpr int NS = TN == 256 ? 4 : (TN == 128 ? 3 : 6);  // ring stages
+    static constexpr int PER_SM = TN == 256 ? 1 : 2;      // CTAs of an SM
     static constexpr uint32_t OFF_SC = NS * STAGE;        // per-warp column scales (columns = tokens)
     static constexpr uint32_t OFF_BAR = OFF_SC + (TOKENS ? 0 : NPW * 2 * CPT * 4);
     static constexpr uint32_t SMEM = OFF_BAR + (2 * NS + 5) * 8 + 16 + 1024;
@@ -61,14 +62,17 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
         "l"(a), "l"(b), "r"(idesc), "n"(ACC)
         : "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t caddr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(caddr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t caddr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(caddr)
+                 : "memory");
     return v;
 }
 
 template <bool TOKENS, int TN, typename TOut>
-__global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), 1) fp8_matmul_tc_kernel(
+__global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::PER_SM)) fp8_matmul_tc_kernel(
     const __grid_constant__ TcArgs p) {
     using C = Cfg<TOKENS, TN>;
     constexpr int NS = C::NS, NPW = C::NPW, CPT = C::CPT;
@@ -119,7 +123,8 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), 1) fp8_matmul_tc_k
                 const int lrow = 128 * (t % p.tiles_l), crow = TN * (t / p.tiles_l);
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const int s = it % NS;
-                    if (it >= NS && !tcf::wait(&empty[s], ((it / NS) - 1) & 1, abort_flag)) break;
+                    if (it >= NS) nap_wait(&empty[s], ((it / NS) - 1) & 1, abort_flag);
+                    if (*abort_flag) break;
                     uint8_t* st = base + s * C::STAGE;
                     tc::mbar_arrive_expect_tx(&full[s], C::STAGE);
                     tc::tma_load_2d(st, &p.lanes, 128 * kb, lrow, &full[s]);
@@ -136,8 +141,8 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), 1) fp8_matmul_tc_k
         for (int t = tile0; t < p.tiles; t += tile_step)
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % NS, b = it & 1;
-                tcf::wait_warp(&full[s], (it / NS) & 1, abort_flag);
-                if (it >= 2) tcf::wait_warp(&acc_free[b], ((it >> 1) - 1) & 1, abort_flag);
+                nap_wait(&full[s], (it / NS) & 1, abort_flag);
+                if (it >= 2) nap_wait(&acc_free[b], ((it >> 1) - 1) & 1, abort_flag);
                 __syncwarp();
                 tc::tc_after_sync();
                 if (tc::elect_one()) {
@@ -195,10 +200,10 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), 1) fp8_matmul_tc_k
                     __syncwarp();
                 }
                 if (kb + 1 < kb1) fetch(kb + 1, nxt);
-                tcf::wait(&acc_full[b], (it >> 1) & 1, abort_flag);
+                nap_wait(&acc_full[b], (it >> 1) & 1, abort_flag);
                 __syncwarp();
                 tc::tc_after_sync();
-                constexpr int STEP = CPT < 32 ? 16 : 32;
+                constexpr int STEP = CPT < 32 || CPT == 64 ? 16 : 32;
 #pragma unroll
                 for (int j = 0; j < CPT; j += STEP) {
                     float v[STEP];
@@ -264,13 +269,37 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), 1) fp8_matmul_tc_k
     if constexpr (!TOKENS) {
         if (split > 1) {
             tc::cluster_sync();
+            // four neighbouring n a thread, every part's loads in flight together
             const int n0 = 128 * (tile0 % p.tiles_l), m0 = TN * (tile0 / p.tiles_l);
             const int toks = g.M - m0 < TN ? g.M - m0 : TN;
-            for (int e = rank * C::THREADS + threadIdx.x; e < toks * 128; e += split * C::THREADS) {
-                const int j = e >> 7, n = n0 + (e & 127);
-                float v = 0.f;
-                for (int r = 0; r < split; ++r) v += ld_cluster_f32(tc::mapa(sbase + 4 * e, (uint32_t)r));
-                if (n < g.N) static_cast<TOut*>(g.out)[(int64_t)(m0 + j) * g.N + n] = from_f32<TOut>(v);
+            TOut* out = static_cast<TOut*>(g.out);
+            const bool whole = n0 + 128 <= g.N && g.N % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+            for (int e = rank * C::THREADS + threadIdx.x; e < toks * 32; e += split * C::THREADS) {
+                const int j = e >> 5, n = n0 + 4 * (e & 31);
+                float4 part[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < split) part[r] = ld_cluster_v4(tc::mapa(sbase + 16 * e, (uint32_t)r));
+                float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < split) {
+                        v[0] += part[r].x;
+                        v[1] += part[r].y;
+                        v[2] += part[r].z;
+                        v[3] += part[r].w;
+                    }
+                TOut* o = out + (int64_t)(m0 + j) * g.N + n;
+                if (whole) {
+                    if constexpr (sizeof(TOut) == 2)
+                        *reinterpret_cast<uint2*>(o) = make_uint2(tc::pack_bf16(v[0], v[1]), tc::pack_bf16(v[2], v[3]));
+                    else
+                        *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (n + i < g.N) o[i] = from_f32<TOut>(v[i]);
+                }
             }
             tc::cluster_sync();  // no CTA leaves while another reads its sums
         }
@@ -337,8 +366,10 @@ inline cudaError_t launch_fp8_matmul(const Args& g, int sms, cudaStream_t st) {
     const int tn = g.M <= 16 ? 16 : (g.M <= 32 ? 32 : (g.M <= 64 ? 64 : 128));
     const int64_t tiles = (int64_t)((g.N + 127) / 128) * ((g.M + tn - 1) / tn);
     const int kb = (g.K + 127) / 128;
+    // as many parts of K, of two blocks at least, as keep every CTA resident (two an SM); a
+    // power of two, since odd clusters leave SMs of a GPC over
     int split = 1;
-    while (split < 8 && tiles * split * 2 <= sms && kb / (split * 2) >= 2) split *= 2;
+    while (split < 8 && tiles * split * 2 <= 2 * sms && kb / (split * 2) >= 2) split *= 2;
     if (tn == 16) return launch_tc<false, 16, TOut>(g, split, sms, st);
     if (tn == 32) return launch_tc<false, 32, TOut>(g, split, sms, st);
     if (tn == 64) return launch_tc<false, 64, TOut>(g, split, sms, st);

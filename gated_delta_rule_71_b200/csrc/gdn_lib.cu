@@ -663,8 +663,26 @@ gdn_status launch_rmsnorm(const gdn::nrm::Args& a, int nt, cudaStream_t st) {
 
 template <typename T, bool VEC>
 gdn_status rmsnorm_sized(const gdn::nrm::Args& a, cudaStream_t st) {
+    // Rows enough for every block of the streamed form to walk a few (eight blocks an SM are
+    // more than shared memory lets in), and three of them in its shared memory.
+    const size_t smem = (size_t)gdn::nrm::kStages * a.D * sizeof(T) * (a.r ? 2 : 1);
+    if (VEC && a.D <= 8192 && smem <= 100 * 1024 && a.rows >= 8 * num_sms()) {
+        auto kern = a.D <= 2048 ? gdn::nrm::rmsnorm_stream_kernel<T, 1>
+                  : a.D <= 4096 ? gdn::nrm::rmsnorm_stream_kernel<T, 2>
+                                : gdn::nrm::rmsnorm_stream_kernel<T, 4>;
+        gdn_status s = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        if (s != GDN_OK) return s;
+        const int per = (int)(200 * 1024 / smem) < 8 ? (int)(200 * 1024 / smem) : 8;
+        const int64_t blocks = (int64_t)num_sms() * (per < 1 ? 1 : per);
+        kern<<<(unsigned)(a.rows < blocks ? a.rows : blocks), 256, smem, st>>>(a);
+        return launch_check();
+    }
+    // The register form: two units a thread for many rows (16384 x 4096 bf16: one 146 us,
+    // two 109, four 161), one for few rows, where latency counts.
     const int units = (a.D + 7) / 8;
-    const int u = units <= 256 ? 1 : (units <= 512 ? 2 : (units <= 4096 ? 4 : 8));
+    int u = a.rows >= 2 * num_sms() ? 2 : 1;
+    while (u < 8 && units > (u == 4 ? 512 : 1024) * u) u *= 2;
+    while (u > 1 && units <= 32 * (u / 2)) u /= 2;
     const int nt = ((units + u - 1) / u + 31) / 32 * 32;
     if (u == 1) return launch_rmsnorm<T, 1, VEC>(a, nt, st);
     if (u == 2) return launch_rmsnorm<T, 2, VEC>(a, nt, st);

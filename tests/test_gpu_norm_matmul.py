@@ -34,7 +34,8 @@ def check_norm(x, w, r, q, sc, r_after, eps=1e-6):
 @pytest.mark.parametrize("ty", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("res", [True, False])
 @pytest.mark.parametrize("rows,D", [(1, 1), (3, 7), (5, 127), (4, 128), (7, 129), (2, 1000), (9, 1001), (3, 2048),
-                                    (2, 4104), (33, 4096), (2, 16384), (1, 16390), (1, 65536), (700, 256)])
+                                    (2, 4104), (33, 4096), (2, 16384), (1, 16390), (1, 65536), (700, 256), (3001, 384), (1300, 4096),
+                                    (1200, 8192), (1250, 2050)])
 def test_norm(cuda_device, rows, D, res, ty):
     g = torch.Generator().manual_seed(D)
     x = torch.randn(rows, D, generator=g).to(ty).cuda()
