@@ -93,10 +93,23 @@ __device__ __forceinline__ bool try_wait_ns(uint32_t bar, uint32_t phase, uint32
     return ok != 0;
 }
 constexpr uint32_t kNap = 20000, kNaps = 1u << 17;  // 20 us a poll, a few seconds in all
+// A phase that is over already costs a plain test (50 cycles, against 120 through the loop).
+__device__ __forceinline__ bool test_phase(uint32_t bar, uint32_t phase) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(phase)
+        : "memory");
+    return ok != 0;
+}
 // Bounded wait of napping polls that honours the CTA's abort flag, and raises it when it
 // gives up.
 __device__ __forceinline__ void nap_wait(uint64_t* bar, uint32_t phase, volatile uint32_t* abort) {
     const uint32_t at = smem_u32(bar);
+    if (test_phase(at, phase)) return;
     uint32_t i = 0;
 #pragma unroll 1
     while (!try_wait_ns(at, phase, kNap)) {
