@@ -29,7 +29,7 @@ constexpr uint32_t kLaneTile = 128 * 128;  // bytes of one 128-row tile of a K b
 
 template <bool TOKENS, int TN>
 struct Cfg {
-    static constexpr int NPW = TN >= 64 ? TN / 16 : 4;    // promotion warps: 64 columns a thread at most
+    static constexpr int NPW = TN == 256 ? 8 : (TN >= 64 ? TN / 16 : 4);    // promotion warps: 64 columns a thread at most
     static constexpr int CPT = TN / (NPW / 4);            // columns of one promotion thread
     static constexpr int THREADS = 32 * (NPW + 2);
     static constexpr uint32_t STAGE = kLaneTile + TN * 128;
@@ -54,12 +54,26 @@ struct TcArgs {
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-template <int ACC>
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+// The products of one K block (four of K = 32; operands at a, b in shared memory, 32 bytes
+// apart) into d, then the arrivals on two barriers when they are done.  Called by a whole
+// converged warp, issued by one elected lane in one sequence: from a branch on the elected
+// lane the same took 500 cycles, as long as the products themselves.
+__device__ __forceinline__ void mma_block_e4m3(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t done0,
+                                               uint32_t done1) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "n"(ACC)
+        "{\n .reg .pred e, z;\n .reg .b32 t;\n .reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n"
+        " mov.b64 a0, {%1, %4};\n mov.b64 b0, {%2, %4};\n"
+        " add.u32 t, %1, 2;\n mov.b64 a1, {t, %4};\n add.u32 t, %2, 2;\n mov.b64 b1, {t, %4};\n"
+        " add.u32 t, %1, 4;\n mov.b64 a2, {t, %4};\n add.u32 t, %2, 4;\n mov.b64 b2, {t, %4};\n"
+        " add.u32 t, %1, 6;\n mov.b64 a3, {t, %4};\n add.u32 t, %2, 6;\n mov.b64 b3, {t, %4};\n"
+        " setp.ne.b32 z, 0, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a0, b0, %3, z;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, 1;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, 1;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, 1;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(tc::desc_hi_sw128()), "r"(done0), "r"(done1)
         : "memory");
 }
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t caddr) {
@@ -137,6 +151,7 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
     } else if (warp == NPW + 1) {
         // ---------------------------------------------------------- MMA warp
         constexpr uint32_t id = idesc_e4m3(128, TN);
+        const uint32_t la0 = tc::desc_lo(sbase, 16), lb0 = tc::desc_lo(sbase + kLaneTile, 16);
         int it = 0;
         for (int t = tile0; t < p.tiles; t += tile_step)
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
@@ -145,17 +160,8 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
                 if (it >= 2) nap_wait(&acc_free[b], ((it >> 1) - 1) & 1, abort_flag);
                 __syncwarp();
                 tc::tc_after_sync();
-                if (tc::elect_one()) {
-                    const uint32_t la = tc::desc_lo(sbase + s * C::STAGE, 16),
-                                   lb = tc::desc_lo(sbase + s * C::STAGE + kLaneTile, 16);
-                    const uint32_t d = tmem + b * TN;
-                    mma_e4m3<0>(d, tc::desc(la), tc::desc(lb), id);
-#pragma unroll
-                    for (int k = 1; k < 4; ++k) mma_e4m3<1>(d, tc::desc(la + 2 * k), tc::desc(lb + 2 * k), id);
-                    tc::mma_commit(&empty[s]);
-                    tc::mma_commit(&acc_full[b]);
-                }
-                __syncwarp();
+                mma_block_e4m3(tmem + b * TN, la0 + s * (C::STAGE / 16), lb0 + s * (C::STAGE / 16), id,
+                               smem_u32(&empty[s]), smem_u32(&acc_full[b]));
             }
         if (tc::elect_one()) {  // never leave with a product in flight
             tc::mma_commit(drain);
@@ -176,30 +182,35 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
             float2 acc[CPT / 2];
 #pragma unroll
             for (int j = 0; j < CPT / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-            // the scales of one block: tokens' by columns, or this lane's token's
-            auto fetch = [&](int kb, float (&v)[NSC]) {
-                const int nb = (TOKENS ? crow : lrow - lane) / 128;
-                const float w = 128 * nb < g.N ? __ldg(g.ws + (int64_t)nb * kb_all + kb) : 0.f;
+            // The scales of one block: the tokens' by columns, or this lane's token's.  They
+            // are fetched a block ahead and multiplied where they are used (a product here
+            // would wait for the loads).
+            const int nb = (TOKENS ? crow : lrow - lane) / 128;
+            const float* pw = 128 * nb < g.N ? g.ws + (int64_t)nb * kb_all : nullptr;
+            const float* pa[NSC];
 #pragma unroll
-                for (int i = 0; i < NSC; ++i) {
-                    const int m = TOKENS ? lrow : crow + lane + 32 * i;
-                    v[i] = (m < g.M && (TOKENS || lane + 32 * i < CPT))
-                               ? w * __ldg(g.as + (int64_t)m * kb_all + kb) : 0.f;
-                }
+            for (int i = 0; i < NSC; ++i) {
+                const int m = TOKENS ? lrow : crow + lane + 32 * i;
+                pa[i] = m < g.M && (TOKENS || lane + 32 * i < CPT) ? g.as + (int64_t)m * kb_all : nullptr;
+            }
+            float nw = 0.f, na[NSC];
+            auto fetch = [&](int kb) {
+                if (pw) nw = __ldg(pw + kb);
+#pragma unroll
+                for (int i = 0; i < NSC; ++i) na[i] = pa[i] ? __ldg(pa[i] + kb) : 0.f;
             };
-            float nxt[NSC];
-            fetch(kb0, nxt);
+            fetch(kb0);
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int b = it & 1;
-                const float s = nxt[0];
+                const float s = nw * na[0];
                 float* scb = sc + b * CPT;
                 if constexpr (!TOKENS) {
 #pragma unroll
                     for (int i = 0; i < NSC; ++i)
-                        if (lane + 32 * i < CPT) scb[lane + 32 * i] = nxt[i];
+                        if (lane + 32 * i < CPT) scb[lane + 32 * i] = nw * na[i];
                     __syncwarp();
                 }
-                if (kb + 1 < kb1) fetch(kb + 1, nxt);
+                if (kb + 1 < kb1) fetch(kb + 1);
                 nap_wait(&acc_full[b], (it >> 1) & 1, abort_flag);
                 __syncwarp();
                 tc::tc_after_sync();
