@@ -31,13 +31,15 @@ template <bool TOKENS, int TN>
 struct Cfg {
     static constexpr int NPW = TN == 256 ? 8 : (TN >= 64 ? TN / 16 : 4);    // promotion warps: 64 columns a thread at most
     static constexpr int CPT = TN / (NPW / 4);            // columns of one promotion thread
+    static constexpr int H = TN == 256 ? 2 : 1;           // column halves, each with its own accumulators and warps
     static constexpr int THREADS = 32 * (NPW + 2);
     static constexpr uint32_t STAGE = kLaneTile + TN * 128;
     static constexpr int NS = TN == 256 ? 4 : (TN == 128 ? 3 : 6);  // ring stages
     static constexpr int PER_SM = TN == 256 ? 1 : 2;      // CTAs of an SM
     static constexpr uint32_t OFF_SC = NS * STAGE;        // per-warp column scales (columns = tokens)
-    static constexpr uint32_t OFF_BAR = OFF_SC + (TOKENS ? 0 : NPW * 2 * CPT * 4);
-    static constexpr uint32_t SMEM = OFF_BAR + (2 * NS + 5) * 8 + 16 + 1024;
+    static constexpr uint32_t OFF_OUT = NS * STAGE;       // per-warp tiles of the result (lanes = tokens)
+    static constexpr uint32_t OFF_BAR = NS * STAGE + (TOKENS ? NPW * 4096 : NPW * 2 * CPT * 4);
+    static constexpr uint32_t SMEM = OFF_BAR + (2 * NS + 4 * H + 1) * 8 + 16 + 1024;
     static constexpr uint32_t COLS = 2 * TN < 32 ? 32 : 2 * TN;
     static_assert(TOKENS || TN * 512 <= NS * STAGE, "partial sums fit in the ring");
     static_assert(SMEM <= 232448, "shared memory budget");
@@ -45,7 +47,9 @@ struct Cfg {
 
 struct TcArgs {
     CUtensorMap lanes, cols;  // [rows, K] e4m3, boxes of 128 bytes x 128 (TN) rows, 128-byte swizzle
+    CUtensorMap out;          // [M, N], boxes of 128 bytes x 32 rows (where out_map)
     Args g;
+    bool out_map;
     int tiles_l, tiles;       // tiles along the lane operand, tiles in all
     int split;                // CTAs of a cluster, each with its part of K
 };
@@ -76,6 +80,15 @@ __device__ __forceinline__ void mma_block_e4m3(uint32_t d, uint32_t a, uint32_t 
         "r"(a), "r"(b), "r"(idesc), "r"(tc::desc_hi_sw128()), "r"(done0), "r"(done1)
         : "memory");
 }
+// Waits for the loads from tensor memory; the values pass through, so no use of them moves
+// before it.
+__device__ __forceinline__ void wait_ld16(float (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t caddr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -89,15 +102,15 @@ template <bool TOKENS, int TN, typename TOut>
 __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::PER_SM)) fp8_matmul_tc_kernel(
     const __grid_constant__ TcArgs p) {
     using C = Cfg<TOKENS, TN>;
-    constexpr int NS = C::NS, NPW = C::NPW, CPT = C::CPT;
+    constexpr int NS = C::NS, NPW = C::NPW, CPT = C::CPT, H = C::H;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     const uint32_t sbase = (raw_u32 + 1023u) & ~1023u;
     uint8_t* base = smem_raw + (sbase - raw_u32);
     uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::OFF_BAR);
-    uint64_t *full = bars, *empty = bars + NS, *acc_full = bars + 2 * NS, *acc_free = acc_full + 2,
-             *drain = acc_full + 4;
-    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * NS + 5);
+    uint64_t *full = bars, *empty = bars + NS, *acc_full = bars + 2 * NS, *acc_free = acc_full + 2 * H,
+             *drain = acc_full + 4 * H;  // accumulator b of half h: [2 h + b]
+    uint32_t* misc = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* abort_flag = misc + 1;
     const Args& g = p.g;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -111,11 +124,11 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], H);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 2 * H; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_free[i], NPW);
+            mbar_init(&acc_free[i], NPW / H);
         }
         mbar_init(drain, 1);
         misc[1] = 0u;
@@ -150,18 +163,22 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
         }
     } else if (warp == NPW + 1) {
         // ---------------------------------------------------------- MMA warp
-        constexpr uint32_t id = idesc_e4m3(128, TN);
+        constexpr uint32_t id = idesc_e4m3(128, TN / H);
         const uint32_t la0 = tc::desc_lo(sbase, 16), lb0 = tc::desc_lo(sbase + kLaneTile, 16);
         int it = 0;
         for (int t = tile0; t < p.tiles; t += tile_step)
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % NS, b = it & 1;
                 nap_wait(&full[s], (it / NS) & 1, abort_flag);
-                if (it >= 2) nap_wait(&acc_free[b], ((it >> 1) - 1) & 1, abort_flag);
-                __syncwarp();
-                tc::tc_after_sync();
-                mma_block_e4m3(tmem + b * TN, la0 + s * (C::STAGE / 16), lb0 + s * (C::STAGE / 16), id,
-                               smem_u32(&empty[s]), smem_u32(&acc_full[b]));
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    if (it >= 2) nap_wait(&acc_free[2 * h + b], ((it >> 1) - 1) & 1, abort_flag);
+                    __syncwarp();
+                    tc::tc_after_sync();
+                    mma_block_e4m3(tmem + b * TN + h * (TN / H), la0 + s * (C::STAGE / 16),
+                                   lb0 + s * (C::STAGE / 16) + h * (TN / H * 128 / 16), id, smem_u32(&empty[s]),
+                                   smem_u32(&acc_full[2 * h + b]));
+                }
             }
         if (tc::elect_one()) {  // never leave with a product in flight
             tc::mma_commit(drain);
@@ -176,6 +193,7 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
         const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + c0;
         float* sc = reinterpret_cast<float*>(base + C::OFF_SC) + warp * 2 * CPT;
         constexpr int NSC = TOKENS ? 1 : (CPT + 31) / 32;  // scales a lane fetches per block
+        const int bar0 = H == 2 ? 2 * (warp >> 2) : 0;
         int it = 0;
         for (int t = tile0; t < p.tiles; t += tile_step) {
             const int lrow = 128 * (t % p.tiles_l) + ln, crow = TN * (t / p.tiles_l) + c0;
@@ -211,53 +229,65 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
                     __syncwarp();
                 }
                 if (kb + 1 < kb1) fetch(kb + 1);
-                nap_wait(&acc_full[b], (it >> 1) & 1, abort_flag);
+                nap_wait(&acc_full[bar0 + b], (it >> 1) & 1, abort_flag);
                 __syncwarp();
                 tc::tc_after_sync();
-                constexpr int STEP = CPT < 32 || CPT == 64 ? 16 : 32;
+                // 16 columns at a time, the next ones under way while these are added
+                float v[2][16];
+                tc::tmem_ld16(taddr + b * TN, v[0]);
 #pragma unroll
-                for (int j = 0; j < CPT; j += STEP) {
-                    float v[STEP];
-                    if constexpr (STEP == 32)
-                        tc::tmem_ld32(taddr + b * TN + j, v);
-                    else
-                        tc::tmem_ld16(taddr + b * TN + j, v);
-                    tc::tmem_wait_ld();
+                for (int j = 0; j < CPT; j += 16) {
+                    wait_ld16(v[(j / 16) & 1]);
+                    if (j + 16 < CPT) tc::tmem_ld16(taddr + b * TN + j + 16, v[(j / 16 + 1) & 1]);
+                    const float* u = v[(j / 16) & 1];
 #pragma unroll
-                    for (int i = 0; i < STEP; i += 2) {
+                    for (int i = 0; i < 16; i += 2) {
                         float2 f;
                         if constexpr (TOKENS)
                             f = make_float2(s, s);
                         else
                             f = *reinterpret_cast<const float2*>(&scb[j + i]);
-                        acc[(j + i) / 2] = __ffma2_rn(make_float2(v[i], v[i + 1]), f, acc[(j + i) / 2]);
+                        acc[(j + i) / 2] = __ffma2_rn(make_float2(u[i], u[i + 1]), f, acc[(j + i) / 2]);
                     }
                 }
                 tc::tc_before_sync();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&acc_free[b]);
+                if (lane == 0) tc::mbar_arrive(&acc_free[bar0 + b]);
             }
             TOut* out = static_cast<TOut*>(g.out);
             if constexpr (TOKENS) {
-                if (lrow < g.M) {
-                    TOut* o = out + (int64_t)lrow * g.N + crow;
-                    constexpr int V = 16 / sizeof(TOut);
-                    if (g.N % V == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0) {
+                if (p.out_map) {
+                    // 32 rows x 128 bytes at a time through this warp's tile: a row a thread
+                    // would write 16 bytes of 32 lines with every store
+                    constexpr int V = 16 / sizeof(TOut), CV = 128 / sizeof(TOut);
+                    uint8_t* stg = base + C::OFF_OUT + warp * 4096;
 #pragma unroll
-                        for (int j = 0; j < CPT; j += V)
-                            if (crow + j < g.N) {
-                                uint4 u;
-                                TOut* e = reinterpret_cast<TOut*>(&u);
+                    for (int j = 0; j < CPT; j += CV) {
+                        if (lane == 0) tc::bulk_wait_read0();
+                        __syncwarp();
 #pragma unroll
-                                for (int i = 0; i < V; ++i)
-                                    e[i] = from_f32<TOut>((i & 1) ? acc[(j + i) / 2].y : acc[(j + i) / 2].x);
-                                *reinterpret_cast<uint4*>(o + j) = u;
+                        for (int k = 0; k < 8; ++k) {
+                            uint4 u;
+                            TOut* e = reinterpret_cast<TOut*>(&u);
+#pragma unroll
+                            for (int i = 0; i < V; ++i) {
+                                const int c = j + k * V + i;
+                                e[i] = from_f32<TOut>((c & 1) ? acc[c / 2].y : acc[c / 2].x);
                             }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < CPT; ++j)
-                            if (crow + j < g.N) o[j] = from_f32<TOut>((j & 1) ? acc[j / 2].y : acc[j / 2].x);
+                            *reinterpret_cast<uint4*>(stg + lane * 128 + ((k ^ (lane & 7)) << 4)) = u;
+                        }
+                        tc::fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && lrow < g.M && crow + j < g.N) {
+                            tc::tma_store_2d(&p.out, smem_u32(stg), crow + j, lrow);
+                            tc::bulk_commit();
+                        }
                     }
+                } else if (lrow < g.M) {
+                    TOut* o = out + (int64_t)lrow * g.N + crow;
+#pragma unroll
+                    for (int j = 0; j < CPT; ++j)
+                        if (crow + j < g.N) o[j] = from_f32<TOut>((j & 1) ? acc[j / 2].y : acc[j / 2].x);
                 }
             } else if (split == 1) {
                 if (lrow < g.N) {
@@ -274,6 +304,7 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
                 for (int j = 0; j < CPT; ++j) red[(c0 + j) * 128 + ln] = (j & 1) ? acc[j / 2].y : acc[j / 2].x;
             }
         }
+        if (TOKENS && lane == 0) tc::bulk_wait_read0();
     }
     tc::tc_before_sync();
     __syncthreads();
@@ -333,6 +364,20 @@ inline bool make_map8(CUtensorMap* m, const void* ptr, int64_t rows, int64_t K, 
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The result: boxes of 128 bytes x 32 rows.
+template <typename TOut>
+inline bool make_map_out(CUtensorMap* m, void* ptr, int64_t rows, int64_t N) {
+    tcf::EncodeTiled enc = tcf::get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)N * sizeof(TOut)};
+    cuuint32_t box[2] = {128u / sizeof(TOut), 32u};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(m, sizeof(TOut) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, ptr, dims,
+               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool TOKENS, int TN, typename TOut>
 inline cudaError_t launch_tc(const Args& g, int split, int sms, cudaStream_t st) {
     using C = Cfg<TOKENS, TN>;
@@ -343,6 +388,8 @@ inline cudaError_t launch_tc(const Args& g, int split, int sms, cudaStream_t st)
                            : make_map8(&p.lanes, g.w, g.N, g.K, g.ldw, 128) &&
                                  make_map8(&p.cols, g.a, g.M, g.K, g.lda, TN);
     if (!ok) return cudaErrorInvalidValue;
+    p.out_map = TOKENS && (int64_t)g.N * sizeof(TOut) % 16 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0;
+    if (p.out_map && !make_map_out<TOut>(&p.out, g.out, g.M, g.N)) return cudaErrorInvalidValue;
     p.g = g;
     const int64_t lanes = TOKENS ? g.M : g.N, cols = TOKENS ? g.N : g.M;
     const int64_t tl = (lanes + 127) / 128, tiles = tl * ((cols + TN - 1) / TN);
