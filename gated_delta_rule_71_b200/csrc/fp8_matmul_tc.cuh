@@ -17,6 +17,18 @@
 // Warps: promotion (4 or 8), then a TMA warp and an MMA warp.  A CTA walks its
 // tiles (blockIdx.x, + gridDim.x, ...): loads and products of the next tile run
 // while the last one is written out.
+//
+// What bounds it and what it measured.
+//  * 4096 x 14336 x 4096, bf16 out: 232 us, 2.07 PFLOP/s.  A K block takes about 990 cycles
+//    an SM, of which the products are 522 (4 x 131) and the promotion, 128 x 256 sums read
+//    from tensor memory and added, some 500 beside waits; the two overlap by half, since only two
+//    256-column accumulators fit in tensor memory.  1792 tiles are 12.1 rounds of 148 SMs,
+//    taken as 13.  Tried: 16 promotion warps of 64 columns 318 us (8 of 128: 292), an
+//    accumulator's loads not ahead of its sums 292 (ahead: 267), rows written a thread
+//    each 267 (through shared memory: 245), accumulators in halves of 128 columns 245
+//    (whole: 232).
+//  * 77 x 6176 x 2064: 11.7 us, 1 x 8192 x 4096: 8.1 us: launch, the ring's first fill and
+//    the cluster's two barriers, then w's bytes at the rate that two CTAs an SM sustain.
 #pragma once
 
 #include "chunk_tc.cuh"
@@ -31,7 +43,6 @@ template <bool TOKENS, int TN>
 struct Cfg {
     static constexpr int NPW = TN == 256 ? 8 : (TN >= 64 ? TN / 16 : 4);    // promotion warps: 64 columns a thread at most
     static constexpr int CPT = TN / (NPW / 4);            // columns of one promotion thread
-    static constexpr int H = TN == 256 ? 2 : 1;           // column halves, each with its own accumulators and warps
     static constexpr int THREADS = 32 * (NPW + 2);
     static constexpr uint32_t STAGE = kLaneTile + TN * 128;
     static constexpr int NS = TN == 256 ? 4 : (TN == 128 ? 3 : 6);  // ring stages
@@ -39,7 +50,7 @@ struct Cfg {
     static constexpr uint32_t OFF_SC = NS * STAGE;        // per-warp column scales (columns = tokens)
     static constexpr uint32_t OFF_OUT = NS * STAGE;       // per-warp tiles of the result (lanes = tokens)
     static constexpr uint32_t OFF_BAR = NS * STAGE + (TOKENS ? NPW * 4096 : NPW * 2 * CPT * 4);
-    static constexpr uint32_t SMEM = OFF_BAR + (2 * NS + 4 * H + 1) * 8 + 16 + 1024;
+    static constexpr uint32_t SMEM = OFF_BAR + (2 * NS + 5) * 8 + 16 + 1024;
     static constexpr uint32_t COLS = 2 * TN < 32 ? 32 : 2 * TN;
     static_assert(TOKENS || TN * 512 <= NS * STAGE, "partial sums fit in the ring");
     static_assert(SMEM <= 232448, "shared memory budget");
@@ -60,8 +71,7 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
 }
 // The products of one K block (four of K = 32; operands at a, b in shared memory, 32 bytes
 // apart) into d, then the arrivals on two barriers when they are done.  Called by a whole
-// converged warp, issued by one elected lane in one sequence: from a branch on the elected
-// lane the same took 500 cycles, as long as the products themselves.
+// converged warp, issued by one elected lane in one sequence.
 __device__ __forceinline__ void mma_block_e4m3(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t done0,
                                                uint32_t done1) {
     asm volatile(
@@ -102,14 +112,14 @@ template <bool TOKENS, int TN, typename TOut>
 __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::PER_SM)) fp8_matmul_tc_kernel(
     const __grid_constant__ TcArgs p) {
     using C = Cfg<TOKENS, TN>;
-    constexpr int NS = C::NS, NPW = C::NPW, CPT = C::CPT, H = C::H;
+    constexpr int NS = C::NS, NPW = C::NPW, CPT = C::CPT;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
     const uint32_t sbase = (raw_u32 + 1023u) & ~1023u;
     uint8_t* base = smem_raw + (sbase - raw_u32);
     uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::OFF_BAR);
-    uint64_t *full = bars, *empty = bars + NS, *acc_full = bars + 2 * NS, *acc_free = acc_full + 2 * H,
-             *drain = acc_full + 4 * H;  // accumulator b of half h: [2 h + b]
+    uint64_t *full = bars, *empty = bars + NS, *acc_full = bars + 2 * NS, *acc_free = acc_full + 2,
+             *drain = acc_full + 4;
     uint32_t* misc = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* abort_flag = misc + 1;
     const Args& g = p.g;
@@ -124,11 +134,11 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], H);
+            mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < 2 * H; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_free[i], NPW / H);
+            mbar_init(&acc_free[i], NPW);
         }
         mbar_init(drain, 1);
         misc[1] = 0u;
@@ -163,22 +173,18 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
         }
     } else if (warp == NPW + 1) {
         // ---------------------------------------------------------- MMA warp
-        constexpr uint32_t id = idesc_e4m3(128, TN / H);
+        constexpr uint32_t id = idesc_e4m3(128, TN);
         const uint32_t la0 = tc::desc_lo(sbase, 16), lb0 = tc::desc_lo(sbase + kLaneTile, 16);
         int it = 0;
         for (int t = tile0; t < p.tiles; t += tile_step)
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % NS, b = it & 1;
                 nap_wait(&full[s], (it / NS) & 1, abort_flag);
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    if (it >= 2) nap_wait(&acc_free[2 * h + b], ((it >> 1) - 1) & 1, abort_flag);
-                    __syncwarp();
-                    tc::tc_after_sync();
-                    mma_block_e4m3(tmem + b * TN + h * (TN / H), la0 + s * (C::STAGE / 16),
-                                   lb0 + s * (C::STAGE / 16) + h * (TN / H * 128 / 16), id, smem_u32(&empty[s]),
-                                   smem_u32(&acc_full[2 * h + b]));
-                }
+                if (it >= 2) nap_wait(&acc_free[b], ((it >> 1) - 1) & 1, abort_flag);
+                __syncwarp();
+                tc::tc_after_sync();
+                mma_block_e4m3(tmem + b * TN, la0 + s * (C::STAGE / 16), lb0 + s * (C::STAGE / 16), id,
+                               smem_u32(&empty[s]), smem_u32(&acc_full[b]));
             }
         if (tc::elect_one()) {  // never leave with a product in flight
             tc::mma_commit(drain);
@@ -193,7 +199,6 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
         const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + c0;
         float* sc = reinterpret_cast<float*>(base + C::OFF_SC) + warp * 2 * CPT;
         constexpr int NSC = TOKENS ? 1 : (CPT + 31) / 32;  // scales a lane fetches per block
-        const int bar0 = H == 2 ? 2 * (warp >> 2) : 0;
         int it = 0;
         for (int t = tile0; t < p.tiles; t += tile_step) {
             const int lrow = 128 * (t % p.tiles_l) + ln, crow = TN * (t / p.tiles_l) + c0;
@@ -229,7 +234,7 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
                     __syncwarp();
                 }
                 if (kb + 1 < kb1) fetch(kb + 1);
-                nap_wait(&acc_full[bar0 + b], (it >> 1) & 1, abort_flag);
+                nap_wait(&acc_full[b], (it >> 1) & 1, abort_flag);
                 __syncwarp();
                 tc::tc_after_sync();
                 // 16 columns at a time, the next ones under way while these are added
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
                 }
                 tc::tc_before_sync();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&acc_free[bar0 + b]);
+                if (lane == 0) tc::mbar_arrive(&acc_free[b]);
             }
             TOut* out = static_cast<TOut*>(g.out);
             if constexpr (TOKENS) {
