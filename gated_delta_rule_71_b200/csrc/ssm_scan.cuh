@@ -79,20 +79,48 @@ __global__ void __launch_bounds__(128) scan_kernel(const ScanArgs a) {
         for (int i = 0; i < 4; ++i)
             st[j][i] = a.h0 ? a.h0[hbase + (int64_t)(16 * j + 4 * s + i) * a.P] : 0.f;
 
+    // one batch of tokens, loaded while the one before it is walked
+    constexpr int NL = kTok * N / 128, XL = kTok * 32 / 128;
+    float rb[NL], rc[NL], rx[XL], rz[XL], rdt = 0.f;
+    auto load = [&](int64_t t0) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int e = tid + 128 * i, t = e / N, n = e - t * N;
+            const bool in = t0 + t < r1;
+            rb[i] = in ? to_f32(Bm[(t0 + t) * a.bs + n]) : 0.f;
+            rc[i] = in ? to_f32(Cm[(t0 + t) * a.cs + n]) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < XL; ++i) {
+            const int64_t t = t0 + (tid >> 5) + 4 * i;
+            rx[i] = t < r1 ? to_f32(x[t * a.xs + (tid & 31)]) : 0.f;
+            rz[i] = z && t < r1 ? to_f32(z[t * a.zs + (tid & 31)]) : 0.f;
+        }
+        if (tid < kTok && t0 + tid < r1) rdt = to_f32(dt[(t0 + tid) * a.dts]);
+    };
+    load(r0);
     for (int64_t t0 = r0; t0 < r1; t0 += kTok) {
         const int nt = (int)(r1 - t0 < kTok ? r1 - t0 : kTok);
-        for (int i = tid; i < nt * N; i += 128) {
-            const int t = i / N, n = i - t * N;
-            sB[t][n] = to_f32(Bm[(t0 + t) * a.bs + n]);
-            sC[t][n] = to_f32(Cm[(t0 + t) * a.cs + n]);
+        float gate[XL];
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int e = tid + 128 * i;
+            (&sB[0][0])[e] = rb[i];
+            (&sC[0][0])[e] = rc[i];
         }
-        for (int i = tid; i < nt * 32; i += 128) sx[i >> 5][i & 31] = to_f32(x[(t0 + (i >> 5)) * a.xs + (i & 31)]);
+#pragma unroll
+        for (int i = 0; i < XL; ++i) {
+            sx[(tid >> 5) + 4 * i][tid & 31] = rx[i];
+            gate[i] = z ? silu_f32(rz[i]) : 1.f;
+        }
         if (tid < nt) {
-            const float d = softplus_f32(to_f32(dt[(t0 + tid) * a.dts]) + bias);
+            const float d = softplus_f32(rdt + bias);
             sdt[tid] = d;
             sa[tid] = expf(A * d);
         }
         __syncthreads();
+        if (t0 + kTok < r1) load(t0 + kTok);
+#pragma unroll 4
         for (int t = 0; t < nt; ++t) {
             const float at = sa[t], u = sdt[t] * sx[t][p];
             float acc0 = 0.f, acc1 = 0.f;
@@ -113,11 +141,13 @@ __global__ void __launch_bounds__(128) scan_kernel(const ScanArgs a) {
             if (s == 0) sy[t][p] = fmaf(Dh, sx[t][p], acc);
         }
         __syncthreads();
-        for (int i = tid; i < nt * 32; i += 128) {
-            const int t = i >> 5, c = i & 31;
-            float v = sy[t][c];
-            if (z) v *= silu_f32(to_f32(z[(t0 + t) * a.zs + c]));
-            y[(t0 + t) * a.H * a.P + c] = from_f32<TIn>(v);
+#pragma unroll
+        for (int i = 0; i < XL; ++i) {
+            const int t = (tid >> 5) + 4 * i;
+            if (t < nt) {
+                const float v = sy[t][tid & 31];
+                y[(t0 + t) * a.H * a.P + (tid & 31)] = from_f32<TIn>(z ? v * gate[i] : v);
+            }
         }
         // the next batch writes sB, sC, sx, sdt, sa only, and those were last read
         // before the barrier above; sy is rewritten after the next one
