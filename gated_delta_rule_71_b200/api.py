@@ -502,6 +502,8 @@ def ssm_scan(x: torch.Tensor, dt: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tens
         _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
         if B != 1:
             raise ValueError("packed sequences need B == 1")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be int32 [n_seq + 1]")
         n_seq = cu_seqlens.numel() - 1
     if h0 is not None:
         _need(h0, "h0", torch.float32, dev)

@@ -19,7 +19,7 @@
 // while the last one is written out.
 //
 // What bounds it and what it measured.
-//  * 4096 x 14336 x 4096, bf16 out: 232 us, 2.07 PFLOP/s.  A K block takes about 990 cycles
+//  * 4096 x 14336 x 4096, bf16 out: 228 us, 2.11 PFLOP/s.  A K block takes about 990 cycles
 //    an SM, of which the products are 522 (4 x 131) and the promotion, 128 x 256 sums read
 //    from tensor memory and added, some 500 beside waits; the two overlap by half, since only two
 //    256-column accumulators fit in tensor memory.  1792 tiles are 12.1 rounds of 148 SMs,
@@ -41,7 +41,7 @@ constexpr uint32_t kLaneTile = 128 * 128;  // bytes of one 128-row tile of a K b
 
 template <bool TOKENS, int TN>
 struct Cfg {
-    static constexpr int NPW = TN == 256 ? 8 : (TN >= 64 ? TN / 16 : 4);    // promotion warps: 64 columns a thread at most
+    static constexpr int NPW = TN >= 128 ? 8 : 4;         // promotion warps: 16 to 128 columns a thread
     static constexpr int CPT = TN / (NPW / 4);            // columns of one promotion thread
     static constexpr int THREADS = 32 * (NPW + 2);
     static constexpr uint32_t STAGE = kLaneTile + TN * 128;

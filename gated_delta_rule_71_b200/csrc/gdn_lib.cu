@@ -822,7 +822,7 @@ gdn_status gdn_rmsnorm_fp8(const void* x, int64_t x_stride, void* residual, int6
     if (rows < 0 || D < 1 || x_stride < D || (residual && r_stride < D) || !(eps >= 0.f))
         return GDN_ERR_INVALID_ARG;
     if (rows == 0) return GDN_OK;
-    if (!x || !weight || !q || !scales || residual == x) return GDN_ERR_INVALID_ARG;
+    if (!x || !weight || !q || !scales || residual == x || q == x || q == residual) return GDN_ERR_INVALID_ARG;
     const size_t es = dtype == GDN_BF16 ? 2 : 4;
     if (!aligned_to(x, es) || !aligned_to(residual, es) || !aligned_to(weight, 4) || !aligned_to(scales, 4))
         return GDN_ERR_INVALID_ARG;
@@ -844,10 +844,10 @@ gdn_status gdn_fp8_matmul(const void* a, int64_t a_stride, const float* a_scales
     if (out_dtype != GDN_F32 && out_dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
     if (M < 0 || N < 1 || K < 1 || a_stride < K || w_stride < K) return GDN_ERR_INVALID_ARG;
     if (M == 0) return GDN_OK;
-    if (!a || !a_scales || !w || !w_scales || !out) return GDN_ERR_INVALID_ARG;
+    if (!a || !a_scales || !w || !w_scales || !out || out == a || out == w) return GDN_ERR_INVALID_ARG;
     if (!aligned_to(a_scales, 4) || !aligned_to(w_scales, 4) || !aligned_to(out, out_dtype == GDN_BF16 ? 2 : 4))
         return GDN_ERR_INVALID_ARG;
-    if (M > 65535 * 64) return GDN_ERR_UNSUPPORTED;
+    if (M > 65535 * 64 || N > (1 << 30) || K > (1 << 30)) return GDN_ERR_UNSUPPORTED;
     const gdn::mm8::Args g{static_cast<const uint8_t*>(a), a_scales, static_cast<const uint8_t*>(w),
                            w_scales, a_stride, w_stride, (int)M, N, K, out};
     cudaStream_t st = as_stream(stream);

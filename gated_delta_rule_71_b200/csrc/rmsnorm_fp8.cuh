@@ -6,10 +6,15 @@
 //     per block of 128 of a row:  scale = max|y| / 448 (1 where that is 0),
 //                                 q = e4m3(y / scale), round to nearest even
 //
-// One block per row, the row in registers between the two passes, so HBM sees
-// each input once and each output once.  A thread owns units of eight
-// consecutive elements; sixteen neighbouring threads hold one block of 128, so
-// its maximum is four shuffles.  Bound by HBM.
+// A block works on a row at a time and holds it in registers between the two
+// passes, so HBM sees each input once and each output once.  A thread owns units of
+// eight consecutive elements; sixteen neighbouring threads hold one block of 128, so
+// its maximum is four shuffles.  Two forms: rows loaded into registers (few rows, any
+// alignment and width), and rows streamed through shared memory (many rows).
+//
+// Many rows are bound by HBM: 16384 x 4096 bf16 with a residual, 87 us, 5.4 TB/s (83 %
+// of a copy's rate).  Few rows are bound by latency: 32 x 2048 2.6 us, of which an
+// empty launch is most; 1111 x 1000 fp32 3.7 us.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -187,7 +192,7 @@ __global__ void __launch_bounds__(U == 4 ? 512 : 1024) rmsnorm_kernel(const Args
 // The same over many rows of moderate width, with the rows streamed through shared memory
 // by bulk copies: a block keeps two rows in flight behind the one it works on, whatever
 // its warps are doing, which the register form cannot (16384 x 4096 bf16 with a residual:
-// 109 us there at its best).  Each thread reads its own units from the stage; the barrier
+// 109 us there at its best, 87 here).  Each thread reads its own units from the stage; the barrier
 // of the row's sum is also the one after which the stage is refilled.
 constexpr int kStages = 3;
 template <typename T, int U>

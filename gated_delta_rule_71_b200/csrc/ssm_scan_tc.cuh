@@ -21,12 +21,24 @@
 // per row and block; inside a block it is taken per pair.
 //
 // A CTA owns 128 value lanes (two heads of 64 or 32 value columns of one group, or
-// one head of 128) of one segment of a sequence.  Twenty warps, each with one job:
+// one head of 128) of one segment of a sequence.  28 warps, each with one job:
 //   X (4)  reads x, writes the split (w x)^T to tensor memory, 32 tokens at a time
-//   M (8)  turns CB into W          S (4)  decays S, hands its bf16 copy to C h
-//   Y (4)  y = Y1 + e^G Y2 + D x, gate, store      gates (2), TMA (1), MMA (1)
-// The tensor pipe is the bound (N = 128: 3300 cycles of products a chunk); the MMA
-// warp orders the products so that each wait falls under another product.
+//   M (8)  turns CB into W          S (4)  makes the gates two chunks ahead; decays S,
+//                                          hands its bf16 copy to C h
+//   Y (8)  e^G Y2, then y = Y1 + that (the skip D x rides on W's diagonal), gate
+//   MMA (2): CB, C h, W x; and the state's products   TMA (2): x, B, C; and z, y tiles
+// x, B, C and z come in and y goes out by TMA tiles; x^T reaches tensor memory by
+// transposing 8 x 8 loads (ldmatrix.trans, st.16x128b).
+//
+// What bounds it: issue slots.  A chunk takes 5700 to 7000 cycles an SM (with a gate:
+// 7000), 60 to 68 % of the slots used: the warps' work on CB, x, S and y is some 5500
+// warp instructions a scheduler, and the gate's silu fills the special-function units.
+// The products (3300 cycles at N = 128) and HBM (a third of its rate) are below that.
+// Measured: 4 x 4096 tokens, H 32, G 8, P 64, N 128, gate: 117 us; 8 packed sequences of
+// 32768 tokens in all, H 32, G 16, P = N = 128: 385 us; one of 131072, H 32, P = N = 64: 520 us
+// (token by token: 4131, 10462 and 58698 us).  Steps that gave most, on the first: z
+// and y through tiles, not a row a thread, 197 to 163; x transposed by its loads and two
+// warpgroups on W, 163 to 153; gates on the S warps and two MMA warps, 143 to 135.
 //
 // Long sequences with few heads are cut into segments: a first launch (STATES)
 // sums each segment's own contribution to the state, a small one chains them, and
@@ -163,6 +175,13 @@ __device__ __forceinline__ int64_t seq_segments(int64_t len, int64_t seg) {
 struct Segment { int seq; int j; int n; int slot; };
 template <bool STATES>
 __device__ __noinline__ bool find_segment(const ScanArgs& a, int64_t k, int64_t seg, int lane, Segment& o) {
+    if (a.cu && seg >= a.T) {  // one segment a sequence (many short ones: no search)
+        if (STATES || k >= a.n_seq) return false;
+        o.seq = (int)k;
+        o.j = o.slot = 0;
+        o.n = 1;
+        return true;
+    }
     if (!a.cu) {
         const int64_t n = seq_segments(a.T, seg), per = STATES ? n - 1 : n;
         if (per == 0 || k >= per * a.n_seq) return false;

@@ -404,10 +404,12 @@ gdn_status gdn_accumulate_f32(float* y, const float* x, int64_t n, void* stream)
  *               that may run at the same time need one each.
  * P, N in {32, 64, 128}.  Sums, decays and states are fp32 in every kernel.
  * Sequences are independent: what one holds, a NaN included, reaches no other.
+ * Within a sequence a NaN or infinity in x reaches y of its head in the whole
+ * block of 128 tokens that holds it (bf16 rows run in blocks), and all later ones.
  * Errors: INVALID_ARG (NULL or misaligned pointers, sizes < 0, H % G != 0, a
  * stride shorter than a row, B != 1 with cu_seqlens, a short workspace),
  * UNSUPPORTED (other P or N).  As in gdn_chunk_fwd, offsets outside [0, T] are
- * undefined behaviour.
+ * undefined behaviour, and so are decreasing ones.
  */
 size_t gdn_ssm_scan_workspace_size(int n_seq, int64_t T_total, int H, int G, int P, int N,
                                    gdn_dtype dtype);
@@ -464,7 +466,7 @@ gdn_status gdn_ssm_decode_step(const void* row, int64_t row_stride, const void* 
  *   residual : `dtype` [rows, D], row stride r_stride, in place; NULL for none;
  *              not x.
  *   weight   : fp32 [D].   q : e4m3 bytes [rows, D].
- *   scales   : fp32 [rows, ceil(D / 128)].
+ *   scales   : fp32 [rows, ceil(D / 128)].  q and scales overlap no input.
  * Errors: INVALID_ARG (NULL or misaligned pointers, sizes, strides, eps < 0),
  * UNSUPPORTED (D > 65536).
  */
@@ -480,10 +482,11 @@ gdn_status gdn_rmsnorm_fp8(const void* x, int64_t x_stride, void* residual, int6
  *   a : e4m3 bytes [M, K], row stride a_stride >= K;   a_scales fp32 [M, ceil(K/128)].
  *   w : e4m3 bytes [N, K], row stride w_stride >= K;
  *       w_scales fp32 [ceil(N/128), ceil(K/128)].
- *   out : [M, N] of out_dtype (GDN_F32 or GDN_BF16), contiguous.
- * M == 0 is a no-op.  Operands whose rows start on 16 bytes run on the tensor
+ *   out : [M, N] of out_dtype (GDN_F32 or GDN_BF16), contiguous; overlaps no input.
+ * The two scales are multiplied first, in fp32.  M == 0 is a no-op.  Operands whose rows start on 16 bytes run on the tensor
  * cores; others on a plain fp32 kernel, much slower.
- * Errors: INVALID_ARG (NULL or misaligned pointers, sizes, strides).
+ * Errors: INVALID_ARG (NULL or misaligned pointers, sizes, strides), UNSUPPORTED
+ * (M > 64 * 65535, N or K > 2^30).
  */
 gdn_status gdn_fp8_matmul(const void* a, int64_t a_stride, const float* a_scales, const void* w,
                           int64_t w_stride, const float* w_scales, int64_t M, int N, int K,

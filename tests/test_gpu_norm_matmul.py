@@ -237,3 +237,66 @@ def test_the_layer(cuda_device):
     full = torch.from_numpy(layer.rmsnorm(both, nw2)[1]) @ wf.T
     assert (out.cpu().double() - full).norm() <= 2.0 ** -4 * full.norm()
     assert gdn.device_status() == 0
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(1300, 1800, 400), (1281, 1805, 272), (2500, 1284, 128), (4097, 600, 1040),
+                                   (300, 16001, 16)])
+def test_matmul_of_prompts(cuda_device, M, N, K, out):
+    # enough tiles of 128 tokens x 256 columns to fill the machine; ends inside a tile, rows of
+    # the result on and off 16 bytes
+    ops = operands(M, N, K, M + N + K)
+    buf = torch.full((M + 2, N), 9.0, dtype=out, device="cuda")
+    r = gdn.fp8_matmul(*ops, out_dtype=out, out=buf[1:M + 1])
+    torch.cuda.synchronize()
+    assert gdn.device_status() == 0
+    check_matmul(ops, r)
+    assert (buf[0] == 9).all() and (buf[M + 1] == 9).all()
+    assert torch.equal(r, gdn.fp8_matmul(*ops, out_dtype=out))
+
+
+def test_norm_streams_and_graph(cuda_device):
+    # the streamed form (many rows) and the register form on two streams at once, then replayed
+    g = torch.Generator().manual_seed(6)
+    sets = []
+    for rows, D in ((2400, 1024), (40, 1024)):
+        sets.append([torch.randn(rows, D, generator=g).bfloat16().cuda() for _ in range(2)] + [torch.ones(D, device="cuda")])
+    want = [(r.clone(), *gdn.rmsnorm_fp8(x, w, residual=r)) for x, r, w in [(x, r.clone(), w) for x, r, w in sets]]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    res = [[r.clone() for _ in range(5)] for _, r, _ in sets]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for i in range(5):
+        for k, (x, _, w) in enumerate(sets):
+            with torch.cuda.stream(streams[k]):
+                got[k] = gdn.rmsnorm_fp8(x, w, residual=res[k][i])
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        assert torch.equal(got[k][0].view(torch.uint8), want[k][1].view(torch.uint8)) and torch.equal(got[k][1], want[k][2])
+    x, r, w = sets[0]
+    live = r.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q, sc = gdn.rmsnorm_fp8(x, w, residual=live)
+    for _ in range(2):
+        live.copy_(r)
+        graph.replay()
+        assert torch.equal(q.view(torch.uint8), want[0][1].view(torch.uint8)) and torch.equal(sc, want[0][2])
+    del graph
+
+
+def test_offsets_behind_two_to_the_31(cuda_device):
+    D, rows = 8192, 262400  # 2^31 elements and more: the last rows are what they are by themselves
+    x = torch.empty(rows, D, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(2))
+    w = torch.ones(D, device="cuda")
+    r = torch.zeros_like(x)
+    q, sc = gdn.rmsnorm_fp8(x, w, residual=r)
+    q1, sc1 = gdn.rmsnorm_fp8(x[-1300:], w, residual=torch.zeros_like(x[-1300:]))
+    assert torch.equal(q[-1300:].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(sc[-1300:], sc1)
+    assert torch.equal(r[-1300:], x[-1300:])
+    del x, r, q
+    a, sa, w, sw = operands(65600, 32776, 16, 8)
+    out = gdn.fp8_matmul(a, sa, w, sw)
+    torch.cuda.synchronize()
+    assert gdn.device_status() == 0
+    check_matmul((a[-40:], sa[-40:], w, sw), out[-40:])

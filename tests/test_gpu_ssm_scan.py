@@ -212,3 +212,33 @@ def test_refusals(cuda_device):
     x = d["x"].expand(2, 8, 2, 64)
     with pytest.raises(ValueError):  # rows of the two sequences are the same memory
         gdn.ssm_scan(x, *(d[k].expand(2, *d[k].shape[1:]) for k in ("dt", "Bm", "Cm")), d["A_log"], d["dt_bias"])
+
+
+@pytest.mark.parametrize("lens", [[(7 * i * i) % 10 for i in range(700)], [(5 * i) % 4 for i in range(300)] + [4000]])
+def test_many_short_sequences(cuda_device, lens):
+    d = make(1, sum(lens), 2, 1, 64, 64, torch.bfloat16, 41, lens)
+    y, hT = gdn.ssm_scan(**d)
+    torch.cuda.synchronize()
+    assert gdn.device_status() == 0
+    check(d, y, hT)
+
+
+def test_rows_behind_two_to_the_31(cuda_device):
+    # y and x pass 2^31 elements; the last sequence is what it is by itself
+    T, H, P = 524416, 32, 128
+    d = make(1, 300, H, 1, P, 64, torch.bfloat16, 43, lens=[300], h0=False)
+    g = torch.Generator("cuda").manual_seed(1)
+    big = {}
+    for k in ("x", "Bm", "Cm", "dt", "z"):
+        t = torch.empty((1, T, *d[k].shape[2:]), dtype=torch.bfloat16, device="cuda")
+        if k == "z":
+            t.fill_(1.0)
+        else:
+            t.normal_(generator=g)
+        t[:, T - 300:] = d[k]
+        big[k] = t
+    y, hT = gdn.ssm_scan(**{**d, **big, "cu_seqlens": torch.tensor([0, T - 300, T], dtype=torch.int32, device="cuda")})
+    y1, h1 = gdn.ssm_scan(**d)
+    assert gdn.device_status() == 0
+    assert torch.equal(y[:, T - 300:], y1) and torch.equal(hT[1:], h1)
+    check(d, y1, h1)

@@ -154,3 +154,36 @@ def test_refusals(cuda_device):
                    dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))):
         with pytest.raises((ValueError, TypeError, gdn._lib.GdnError)):
             gdn.ssm_decode_step(**{**d, **change})
+
+
+def test_slots_behind_two_to_the_31(cuda_device):
+    H, G, P, N, slots = 32, 1, 128, 128, 4200  # 2^19 states a slot
+    d = make(3, 4, H, G, P, N, seed=12)
+    small = clone(d)
+    C = d["conv_w"].shape[0]
+    state = torch.empty(slots, H, N, P, device="cuda")
+    conv = torch.empty(slots, C, 3, dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([4199, 4097, 0], dtype=torch.int32, device="cuda")
+    state[at.long()], conv[at.long()] = d["state"][:3], d["conv_state"][:3]
+    y = gdn.ssm_decode_step(**{**d, "state": state, "conv_state": conv, "state_indices": at})
+    ref = gdn.ssm_decode_step(**small)
+    assert torch.equal(y, ref) and torch.equal(state[at.long()], small["state"][:3])
+    assert torch.equal(conv[at.long()], small["conv_state"][:3])
+
+
+def test_two_calls_at_once(cuda_device):
+    sets = [make(64, 64, 8, 2, 64, 128, seed=s) for s in (21, 22)]
+    refs = [clone(d) for d in sets]
+    for r in refs:
+        r["y"] = [gdn.ssm_decode_step(**{k: v for k, v in r.items() if k != "y"}) for _ in range(4)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for k, d in enumerate(sets):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(gdn.ssm_decode_step(**d))
+    torch.cuda.synchronize()
+    for k, d in enumerate(sets):
+        assert all(torch.equal(a, b) for a, b in zip(got[k], refs[k]["y"]))
+        assert torch.equal(d["state"], refs[k]["state"]) and torch.equal(d["conv_state"], refs[k]["conv_state"])

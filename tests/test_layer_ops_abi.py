@@ -84,7 +84,8 @@ def test_norm_refusals():
         return f(x, xs, r, rs, ty, w, eps, rows, D, out, sc, None)
     for bad in (dict(ty=2), dict(rows=-1), dict(D=0), dict(xs=63), dict(r=q, rs=63), dict(eps=-1.0),
                 dict(eps=float("nan")), dict(x=None), dict(w=None), dict(out=None), dict(sc=None),
-                dict(r=p, rs=64), dict(x=ctypes.c_void_p(257)), dict(sc=ctypes.c_void_p(258))):
+                dict(r=p, rs=64), dict(x=ctypes.c_void_p(257)), dict(sc=ctypes.c_void_p(258)), dict(out=p),
+                dict(r=q, rs=64)):
         assert norm(**bad) == INVALID, bad
     assert norm(D=65537, xs=65537) == UNSUPPORTED
     assert norm(rows=0) == OK
@@ -97,10 +98,12 @@ def test_matmul_refusals():
         return f(a, lda, sa, w, ldw, sw, M, N, K, out, ty, None)
     for bad in (dict(M=-1), dict(N=0), dict(K=0), dict(lda=63), dict(ldw=63), dict(a=None), dict(w=None),
                 dict(sa=None), dict(sw=None), dict(out=None), dict(ty=3), dict(sa=ctypes.c_void_p(258)),
-                dict(out=ctypes.c_void_p(513))):
+                dict(out=ctypes.c_void_p(513)), dict(out=p), dict(a=q)):
         assert mm(**bad) == INVALID, bad
     assert mm(M=0) == OK
     assert mm(M=1 << 40) == UNSUPPORTED
+    assert mm(N=(1 << 30) + 1) == UNSUPPORTED
+    assert mm(K=(1 << 30) + 1, lda=1 << 31, ldw=1 << 31) == UNSUPPORTED
 
 
 def test_the_binding_refuses_host_tensors():
