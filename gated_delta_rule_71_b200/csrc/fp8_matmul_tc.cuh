@@ -19,16 +19,18 @@
 // while the last one is written out.
 //
 // What bounds it and what it measured.
-//  * 4096 x 14336 x 4096, bf16 out: 228 us, 2.11 PFLOP/s.  A K block takes about 990 cycles
-//    an SM, of which the products are 522 (4 x 131) and the promotion, 128 x 256 sums read
-//    from tensor memory and added, some 500 beside waits; the two overlap by half, since only two
+//  * 4096 x 14336 x 4096, bf16 out: 225 us, 2.14 PFLOP/s.  A K block takes about 960 cycles
+//    an SM, of which the products are 522 (4 x 131); reading 128 x 256 sums from tensor
+//    memory and adding them some 500 beside waits; the two overlap by half, since only two
 //    256-column accumulators fit in tensor memory.  1792 tiles are 12.1 rounds of 148 SMs,
-//    taken as 13.  Tried: 16 promotion warps of 64 columns 318 us (8 of 128: 292), an
-//    accumulator's loads not ahead of its sums 292 (ahead: 267), rows written a thread
-//    each 267 (through shared memory: 245), accumulators in halves of 128 columns 245
-//    (whole: 232).
-//  * 77 x 6176 x 2064: 11.7 us, 1 x 8192 x 4096: 8.1 us: launch, the ring's first fill and
-//    the cluster's two barriers, then w's bytes at the rate that two CTAs an SM sustain.
+//    taken as 13.  The promotion warps have 168 registers for 128 sums and 32 loaded
+//    ones (ten warps are three on some scheduler), so a few more live values cost a tenth.
+//    Tried: 16 promotion warps of 64 columns 318 us (8 of 128: 292), an accumulator's
+//    loads not ahead of its sums 292 (ahead: 267), rows written a thread each 267 (through
+//    shared memory: 245), accumulators in halves of 128 columns 245 (whole: 232).
+//  * 77 x 6176 x 2064: 11.1 us, 1 x 8192 x 4096: 8.4 us, 64 x 8192 x 4096: 11.8 us: launch, the
+//    ring's first fill and the cluster's barriers, then w's bytes at the rate that two CTAs
+//    an SM sustain (one an SM, 17.7 us for the last).
 #pragma once
 
 #include "chunk_tc.cuh"
@@ -45,22 +47,21 @@ struct Cfg {
     static constexpr int CPT = TN / (NPW / 4);            // columns of one promotion thread
     static constexpr int THREADS = 32 * (NPW + 2);
     static constexpr uint32_t STAGE = kLaneTile + TN * 128;
-    static constexpr int NS = TN == 256 ? 4 : (TN == 128 ? 3 : 6);  // ring stages
+    static constexpr int NS = TN == 256 ? 4 : (TN == 128 ? 3 : (TN == 64 ? 4 : 5));  // ring stages
     static constexpr int PER_SM = TN == 256 ? 1 : 2;      // CTAs of an SM
-    static constexpr uint32_t OFF_SC = NS * STAGE;        // per-warp column scales (columns = tokens)
+    static constexpr uint32_t OFF_SC = NS * STAGE;        // [2][TN] column scales (columns = tokens)
     static constexpr uint32_t OFF_OUT = NS * STAGE;       // per-warp tiles of the result (lanes = tokens)
-    static constexpr uint32_t OFF_BAR = NS * STAGE + (TOKENS ? NPW * 4096 : NPW * 2 * CPT * 4);
+    static constexpr uint32_t OFF_BAR = NS * STAGE + (TOKENS ? NPW * 4096 : 2 * TN * 4);
     static constexpr uint32_t SMEM = OFF_BAR + (2 * NS + 5) * 8 + 16 + 1024;
     static constexpr uint32_t COLS = 2 * TN < 32 ? 32 : 2 * TN;
     static_assert(TOKENS || TN * 512 <= NS * STAGE, "partial sums fit in the ring");
-    static_assert(SMEM <= 232448, "shared memory budget");
+    static_assert(SMEM <= (PER_SM == 1 ? 232448 : 115712), "shared memory budget");
 };
 
 struct TcArgs {
     CUtensorMap lanes, cols;  // [rows, K] e4m3, boxes of 128 bytes x 128 (TN) rows, 128-byte swizzle
-    CUtensorMap out;          // [M, N], boxes of 128 bytes x 32 rows (where out_map)
+    CUtensorMap out;          // [M, N], boxes of 128 bytes x 32 rows (MAP)
     Args g;
-    bool out_map;
     int tiles_l, tiles;       // tiles along the lane operand, tiles in all
     int split;                // CTAs of a cluster, each with its part of K
 };
@@ -108,7 +109,9 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t caddr) {
     return v;
 }
 
-template <bool TOKENS, int TN, typename TOut>
+// MAP: the result's rows start on 16 bytes, and its tiles leave by TMA (lanes = tokens; with
+// both ways in one kernel the sums spill: 228 to 241 us).
+template <bool TOKENS, int TN, typename TOut, bool MAP>
 __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::PER_SM)) fp8_matmul_tc_kernel(
     const __grid_constant__ TcArgs p) {
     using C = Cfg<TOKENS, TN>;
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_full[i], TOKENS ? 1 : 2);  // the products (, their scales)
             mbar_init(&acc_free[i], NPW);
         }
         mbar_init(drain, 1);
@@ -175,17 +178,55 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
         // ---------------------------------------------------------- MMA warp
         constexpr uint32_t id = idesc_e4m3(128, TN);
         const uint32_t la0 = tc::desc_lo(sbase, 16), lb0 = tc::desc_lo(sbase + kLaneTile, 16);
+        auto products = [&](int it) {
+            const int s = it % NS, b = it & 1;
+            nap_wait(&full[s], (it / NS) & 1, abort_flag);
+            if (it >= 2) nap_wait(&acc_free[b], ((it >> 1) - 1) & 1, abort_flag);
+            __syncwarp();
+            tc::tc_after_sync();
+            mma_block_e4m3(tmem + b * TN, la0 + s * (C::STAGE / 16), lb0 + s * (C::STAGE / 16), id,
+                           smem_u32(&empty[s]), smem_u32(&acc_full[b]));
+        };
         int it = 0;
-        for (int t = tile0; t < p.tiles; t += tile_step)
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const int s = it % NS, b = it & 1;
-                nap_wait(&full[s], (it / NS) & 1, abort_flag);
-                if (it >= 2) nap_wait(&acc_free[b], ((it >> 1) - 1) & 1, abort_flag);
-                __syncwarp();
-                tc::tc_after_sync();
-                mma_block_e4m3(tmem + b * TN, la0 + s * (C::STAGE / 16), lb0 + s * (C::STAGE / 16), id,
-                               smem_u32(&empty[s]), smem_u32(&acc_full[b]));
+        if constexpr (TOKENS) {
+            for (int t = tile0; t < p.tiles; t += tile_step)
+                for (int kb = kb0; kb < kb1; ++kb, ++it) products(it);
+        } else {
+            // This warp also hands out the scales of a block's columns (ws as), behind its
+            // products: loaded two blocks ahead, in place of those of two blocks ago, whose
+            // sums are done.  (In the promotion warps, one block ahead, the loads cost 128
+            // tokens their registers and their time.)
+            constexpr int NC = (TN + 31) / 32;
+            float* sc = reinterpret_cast<float*>(base + C::OFF_SC);
+            for (int t = tile0; t < p.tiles; t += tile_step) {
+                const int nb = t % p.tiles_l, m0 = TN * (t / p.tiles_l) + lane;
+                const float* pw = g.ws + (int64_t)nb * kb_all;
+                const float* pa = g.as + (int64_t)m0 * kb_all;
+                float nw[2], na[2][NC];
+                auto fetch = [&](int kb, int u) {
+                    nw[u] = kb < kb1 ? __ldg(pw + kb) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < NC; ++i)
+                        na[u][i] = kb < kb1 && m0 + 32 * i < g.M && lane + 32 * i < TN
+                                       ? __ldg(pa + (int64_t)32 * i * kb_all + kb) : 0.f;
+                };
+                fetch(kb0, 0);
+                fetch(kb0 + 1, 1);
+                for (int kbu = kb0; kbu < kb1; kbu += 2)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        if (kbu + u < kb1) {
+                            products(it);
+#pragma unroll
+                            for (int i = 0; i < NC; ++i)
+                                if (lane + 32 * i < TN) sc[(it & 1) * TN + lane + 32 * i] = nw[u] * na[u][i];
+                            __syncwarp();
+                            if (lane == 0) tc::mbar_arrive(&acc_full[it & 1]);
+                            fetch(kbu + u + 2, u);
+                            ++it;
+                        }
             }
+        }
         if (tc::elect_one()) {  // never leave with a product in flight
             tc::mma_commit(drain);
             tcf::drain_wait(drain, 0);
@@ -197,42 +238,30 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
         const int c0 = CPT * (warp >> 2);          // first column of this thread
         const int ln = 32 * q + lane;
         const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + c0;
-        float* sc = reinterpret_cast<float*>(base + C::OFF_SC) + warp * 2 * CPT;
-        constexpr int NSC = TOKENS ? 1 : (CPT + 31) / 32;  // scales a lane fetches per block
+        const float* sc = reinterpret_cast<const float*>(base + C::OFF_SC) + c0;
         int it = 0;
         for (int t = tile0; t < p.tiles; t += tile_step) {
             const int lrow = 128 * (t % p.tiles_l) + ln, crow = TN * (t / p.tiles_l) + c0;
             float2 acc[CPT / 2];
 #pragma unroll
             for (int j = 0; j < CPT / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-            // The scales of one block: the tokens' by columns, or this lane's token's.  They
-            // are fetched a block ahead and multiplied where they are used (a product here
-            // would wait for the loads).
-            const int nb = (TOKENS ? crow : lrow - lane) / 128;
-            const float* pw = 128 * nb < g.N ? g.ws + (int64_t)nb * kb_all : nullptr;
-            const float* pa[NSC];
-#pragma unroll
-            for (int i = 0; i < NSC; ++i) {
-                const int m = TOKENS ? lrow : crow + lane + 32 * i;
-                pa[i] = m < g.M && (TOKENS || lane + 32 * i < CPT) ? g.as + (int64_t)m * kb_all : nullptr;
-            }
-            float nw = 0.f, na[NSC];
+            // Lanes are tokens: this token's scale of a block is fetched a block ahead and multiplied
+            // where it is used (a product here would wait for the loads).  Rows behind M and N
+            // take the first one's: nothing of theirs is stored.
+            const float* pw = g.ws + (int64_t)(TOKENS && crow < g.N ? crow / 128 : 0) * kb_all;
+            const float* pa = g.as + (int64_t)(TOKENS && lrow < g.M ? lrow : 0) * kb_all;
+            float nw = 0.f, na = 0.f;
             auto fetch = [&](int kb) {
-                if (pw) nw = __ldg(pw + kb);
-#pragma unroll
-                for (int i = 0; i < NSC; ++i) na[i] = pa[i] ? __ldg(pa[i] + kb) : 0.f;
+                if constexpr (TOKENS) {
+                    nw = __ldg(pw + kb);
+                    na = __ldg(pa + kb);
+                }
             };
             fetch(kb0);
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int b = it & 1;
-                const float s = nw * na[0];
-                float* scb = sc + b * CPT;
-                if constexpr (!TOKENS) {
-#pragma unroll
-                    for (int i = 0; i < NSC; ++i)
-                        if (lane + 32 * i < CPT) scb[lane + 32 * i] = nw * na[i];
-                    __syncwarp();
-                }
+                const float s = nw * na;
+                const float* scb = sc + b * TN;
                 if (kb + 1 < kb1) fetch(kb + 1);
                 nap_wait(&acc_full[b], (it >> 1) & 1, abort_flag);
                 __syncwarp();
@@ -261,38 +290,43 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
             }
             TOut* out = static_cast<TOut*>(g.out);
             if constexpr (TOKENS) {
-                if (p.out_map) {
-                    // 32 rows x 128 bytes at a time through this warp's tile: a row a thread
-                    // would write 16 bytes of 32 lines with every store
-                    constexpr int V = 16 / sizeof(TOut), CV = 128 / sizeof(TOut);
-                    uint8_t* stg = base + C::OFF_OUT + warp * 4096;
+                // 32 rows x 128 bytes at a time through this warp's tile: a row a thread would
+                // write 16 bytes (or one element) of 32 lines with every store
+                constexpr int V = 16 / sizeof(TOut), CV = 128 / sizeof(TOut);
+                uint8_t* stg = base + C::OFF_OUT + warp * 4096;
 #pragma unroll
-                    for (int j = 0; j < CPT; j += CV) {
-                        if (lane == 0) tc::bulk_wait_read0();
-                        __syncwarp();
+                for (int j = 0; j < CPT; j += CV) {
+                    if (MAP && lane == 0) tc::bulk_wait_read0();
+                    __syncwarp();
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            uint4 u;
-                            TOut* e = reinterpret_cast<TOut*>(&u);
+                    for (int k = 0; k < 8; ++k) {
+                        uint4 u;
+                        TOut* e = reinterpret_cast<TOut*>(&u);
 #pragma unroll
-                            for (int i = 0; i < V; ++i) {
-                                const int c = j + k * V + i;
-                                e[i] = from_f32<TOut>((c & 1) ? acc[c / 2].y : acc[c / 2].x);
-                            }
-                            *reinterpret_cast<uint4*>(stg + lane * 128 + ((k ^ (lane & 7)) << 4)) = u;
+                        for (int i = 0; i < V; ++i) {
+                            const int c = j + k * V + i;
+                            e[i] = from_f32<TOut>((c & 1) ? acc[c / 2].y : acc[c / 2].x);
                         }
+                        *reinterpret_cast<uint4*>(stg + lane * 128 + ((k ^ (lane & 7)) << 4)) = u;
+                    }
+                    if constexpr (MAP) {
                         tc::fence_async_smem();
                         __syncwarp();
                         if (lane == 0 && lrow < g.M && crow + j < g.N) {
                             tc::tma_store_2d(&p.out, smem_u32(stg), crow + j, lrow);
                             tc::bulk_commit();
                         }
-                    }
-                } else if (lrow < g.M) {
-                    TOut* o = out + (int64_t)lrow * g.N + crow;
+                    } else {  // rows that do not start on 16 bytes: a row of the tile a warp's store
+                        __syncwarp();
+                        const int rows = g.M - (lrow - lane), left = g.N - crow - j;
+#pragma unroll 4
+                        for (int r = 0; r < 32; ++r)
 #pragma unroll
-                    for (int j = 0; j < CPT; ++j)
-                        if (crow + j < g.N) o[j] = from_f32<TOut>((j & 1) ? acc[j / 2].y : acc[j / 2].x);
+                            for (int c = 0; c < CV; c += 32)
+                                if (r < rows && c + lane < left)
+                                    out[(int64_t)(lrow - lane + r) * g.N + crow + j + c + lane] =
+                                        reinterpret_cast<const TOut*>(stg + r * 128 + ((((c + lane) / V) ^ (r & 7)) << 4))[lane % V];
+                    }
                 }
             } else if (split == 1) {
                 if (lrow < g.N) {
@@ -309,7 +343,7 @@ __global__ void __launch_bounds__((Cfg<TOKENS, TN>::THREADS), (Cfg<TOKENS, TN>::
                 for (int j = 0; j < CPT; ++j) red[(c0 + j) * 128 + ln] = (j & 1) ? acc[j / 2].y : acc[j / 2].x;
             }
         }
-        if (TOKENS && lane == 0) tc::bulk_wait_read0();
+        if (MAP && lane == 0) tc::bulk_wait_read0();
     }
     tc::tc_before_sync();
     __syncthreads();
@@ -383,7 +417,7 @@ inline bool make_map_out(CUtensorMap* m, void* ptr, int64_t rows, int64_t N) {
                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool TOKENS, int TN, typename TOut>
+template <bool TOKENS, int TN, typename TOut, bool MAP = false>
 inline cudaError_t launch_tc(const Args& g, int split, int sms, cudaStream_t st) {
     using C = Cfg<TOKENS, TN>;
     TcArgs p;
@@ -393,8 +427,7 @@ inline cudaError_t launch_tc(const Args& g, int split, int sms, cudaStream_t st)
                            : make_map8(&p.lanes, g.w, g.N, g.K, g.ldw, 128) &&
                                  make_map8(&p.cols, g.a, g.M, g.K, g.lda, TN);
     if (!ok) return cudaErrorInvalidValue;
-    p.out_map = TOKENS && (int64_t)g.N * sizeof(TOut) % 16 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0;
-    if (p.out_map && !make_map_out<TOut>(&p.out, g.out, g.M, g.N)) return cudaErrorInvalidValue;
+    if (MAP && !make_map_out<TOut>(&p.out, g.out, g.M, g.N)) return cudaErrorInvalidValue;
     p.g = g;
     const int64_t lanes = TOKENS ? g.M : g.N, cols = TOKENS ? g.N : g.M;
     const int64_t tl = (lanes + 127) / 128, tiles = tl * ((cols + TN - 1) / TN);
@@ -402,7 +435,7 @@ inline cudaError_t launch_tc(const Args& g, int split, int sms, cudaStream_t st)
     p.tiles_l = (int)tl;
     p.tiles = (int)tiles;
     p.split = split;
-    auto kern = fp8_matmul_tc_kernel<TOKENS, TN, TOut>;
+    auto kern = fp8_matmul_tc_kernel<TOKENS, TN, TOut, MAP>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
@@ -425,7 +458,10 @@ inline cudaError_t launch_tc(const Args& g, int split, int sms, cudaStream_t st)
 template <typename TOut>
 inline cudaError_t launch_fp8_matmul(const Args& g, int sms, cudaStream_t st) {
     const int64_t tok_tiles = (int64_t)((g.M + 127) / 128) * ((g.N + 255) / 256);
-    if (g.M > 128 && tok_tiles >= sms / 2) return launch_tc<true, 256, TOut>(g, 1, sms, st);
+    if (g.M > 128 && tok_tiles >= sms / 2) {
+        const bool map = (int64_t)g.N * sizeof(TOut) % 16 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15u) == 0;
+        return map ? launch_tc<true, 256, TOut, true>(g, 1, sms, st) : launch_tc<true, 256, TOut, false>(g, 1, sms, st);
+    }
     const int tn = g.M <= 16 ? 16 : (g.M <= 32 ? 32 : (g.M <= 64 ? 64 : 128));
     const int64_t tiles = (int64_t)((g.N + 127) / 128) * ((g.M + tn - 1) / tn);
     const int kb = (g.K + 127) / 128;

@@ -9,6 +9,7 @@
 #include <cstring>
 #include <mutex>
 #include <type_traits>
+#include <type_traits>
 
 #include "gdn.h"
 #include "common.cuh"
@@ -663,6 +664,16 @@ gdn_status launch_rmsnorm(const gdn::nrm::Args& a, int nt, cudaStream_t st) {
 
 template <typename T, bool VEC>
 gdn_status rmsnorm_sized(const gdn::nrm::Args& a, cudaStream_t st) {
+    // Many narrow rows: a row a warp (bf16 with a residual: 90511 x 240 44 us against 115,
+    // 40000 x 512 38 against 58; 20000 x 1000 44 against 39, so no wider; element by element
+    // 90511 x 241 150 against 91, so not those).
+    if (VEC && a.D <= 512 && a.rows >= 8 * num_sms()) {
+        const int64_t most = (int64_t)num_sms() * 8, need = (a.rows + 7) / 8;
+        const unsigned blocks = (unsigned)(need < most ? need : most);
+        if (a.D <= 256) gdn::nrm::rmsnorm_warp_kernel<T, 1><<<blocks, 256, 0, st>>>(a);
+        else gdn::nrm::rmsnorm_warp_kernel<T, 2><<<blocks, 256, 0, st>>>(a);
+        return launch_check();
+    }
     // Rows enough for every block of the streamed form to walk a few (eight blocks an SM are
     // more than shared memory lets in), and three of them in its shared memory.
     const size_t smem = (size_t)gdn::nrm::kStages * a.D * sizeof(T) * (a.r ? 2 : 1);
@@ -789,7 +800,7 @@ gdn_status gdn_ssm_decode_step(const void* row, int64_t row_stride, const void* 
     if (!workspace || ws_bytes < gdn_ssm_decode_step_workspace_size(n, H, G, P, N) || !aligned16(workspace))
         return GDN_ERR_INVALID_ARG;
     if ((int64_t)n * H * 2 > 0x7fffffff || C > 0x7fffffff / 4 ||
-        n > 65535 * gdn::ssm::kDecReqs)
+        n > 65535 * gdn::ssm::kDecVecReqs)
         return GDN_ERR_UNSUPPORTED;
     using bf = __nv_bfloat16;
     const gdn::ssm::DecodeArgs a{(const bf*)row, (const bf*)dt, (const bf*)z, row_stride, dt_stride,
@@ -797,12 +808,23 @@ gdn_status gdn_ssm_decode_step(const void* row, int64_t row_stride, const void* 
                                  activation, n, n_slots, (int)C, A_log, dt_bias, D, H, G, state,
                                  static_cast<float*>(workspace), (bf*)y};
     cudaStream_t st = as_stream(stream);
-    const dim3 grid((unsigned)((C + 127) / 128), (unsigned)((n + gdn::ssm::kDecReqs - 1) / gdn::ssm::kDecReqs));
+    const auto conv = [&](auto w) {
+        constexpr int TAPS = decltype(w)::value;
+        // many requests: 16-byte accesses (256 requests, all: 190 us before, 187); few: a channel a
+        // thread has the shorter way (one request: 4.4 against 5.1)
+        if (n >= 64 && aligned16(row) && row_stride % 8 == 0 && aligned16(conv_state) && aligned16(conv_w)) {
+            const dim3 grid((unsigned)((C / 8 + 127) / 128), (unsigned)((n + gdn::ssm::kDecVecReqs - 1) / gdn::ssm::kDecVecReqs));
+            gdn::ssm::decode_conv_vec_kernel<TAPS><<<grid, 128, 0, st>>>(a);
+        } else {
+            const dim3 grid((unsigned)((C + 127) / 128), (unsigned)((n + gdn::ssm::kDecReqs - 1) / gdn::ssm::kDecReqs));
+            gdn::ssm::decode_conv_kernel<TAPS><<<grid, 128, 0, st>>>(a);
+        }
+    };
     switch (W) {
-        case 1: gdn::ssm::decode_conv_kernel<1><<<grid, 128, 0, st>>>(a); break;
-        case 2: gdn::ssm::decode_conv_kernel<2><<<grid, 128, 0, st>>>(a); break;
-        case 3: gdn::ssm::decode_conv_kernel<3><<<grid, 128, 0, st>>>(a); break;
-        default: gdn::ssm::decode_conv_kernel<4><<<grid, 128, 0, st>>>(a); break;
+        case 1: conv(std::integral_constant<int, 1>()); break;
+        case 2: conv(std::integral_constant<int, 2>()); break;
+        case 3: conv(std::integral_constant<int, 3>()); break;
+        default: conv(std::integral_constant<int, 4>()); break;
     }
     gdn_status s = launch_check();
     if (s != GDN_OK) return s;

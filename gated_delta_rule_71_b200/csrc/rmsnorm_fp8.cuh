@@ -8,9 +8,10 @@
 //
 // A block works on a row at a time and holds it in registers between the two
 // passes, so HBM sees each input once and each output once.  A thread owns units of
-// eight consecutive elements; sixteen neighbouring threads hold one block of 128, so
-// its maximum is four shuffles.  Two forms: rows loaded into registers (few rows, any
-// alignment and width), and rows streamed through shared memory (many rows).
+// eight elements, consecutive ones where rows allow 16-byte accesses: sixteen neighbouring
+// threads hold one block of 128, so its maximum is four shuffles.  Three forms: a row a block in
+// registers (few rows, any alignment and width), rows streamed through shared memory
+// (many rows), and a row a warp (many narrow rows).
 //
 // Many rows are bound by HBM: 16384 x 4096 bf16 with a residual, 87 us, 5.4 TB/s (83 %
 // of a copy's rate).  Few rows are bound by latency: 32 x 2048 2.6 us, of which an
@@ -44,7 +45,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return m;
 }
 
-// Eight consecutive elements.  VEC: 16-byte accesses, all eight in the row.
+// A thread's units of eight elements: unit i starts at first<VEC>(i).  VEC: eight consecutive
+// ones by 16-byte accesses, all in the row.  Else every 32nd of the 256 that the warp's unit
+// covers, so that element by element a warp still touches consecutive ones (bf16, with a
+// residual: 90511 x 241 71 us, 8000 x 2050 69; consecutive ones a thread: 91 and 73).
+template <bool VEC>
+__device__ __forceinline__ int first(int i, int tid, int nt) {
+    return VEC ? 8 * (tid + i * nt) : 256 * ((tid >> 5) + i * (nt >> 5)) + (tid & 31);
+}
 template <typename T, bool VEC>
 __device__ __forceinline__ void load8(const T* p, int left, float (&v)[8]) {
     if constexpr (VEC) {
@@ -56,7 +64,7 @@ __device__ __forceinline__ void load8(const T* p, int left, float (&v)[8]) {
         for (int i = 0; i < 8; ++i) v[i] = to_f32(reinterpret_cast<const T*>(u)[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < left ? to_f32(p[i]) : 0.f;
+        for (int i = 0; i < 8; ++i) v[i] = 32 * i < left ? to_f32(p[32 * i]) : 0.f;
     }
 }
 template <typename T, bool VEC>
@@ -71,7 +79,7 @@ __device__ __forceinline__ void store8(T* p, int left, const float (&v)[8]) {
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < left) p[i] = from_f32<T>(v[i]);
+            if (32 * i < left) p[32 * i] = from_f32<T>(v[i]);
     }
 }
 
@@ -81,29 +89,34 @@ __device__ __forceinline__ void write_row(const Args& a, int64_t row, float (&v)
     const int D = a.D, nblk = (D + 127) / 128;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const int e = 8 * (tid + i * nt), left = D - e;
-        float m = 0.f;
+        const int e = first<VEC>(i, tid, nt), left = D - e;
+        float m[2] = {0.f, 0.f};  // of the unit's block; else of its two
         if (left > 0) {
             float w[8];
             load8<float, VEC>(a.w + e, left, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[i][j] = v[i][j] * rstd * w[j];
-                m = max_nan(m, fabsf(v[i][j]));
+                m[VEC ? 0 : j / 4] = max_nan(m[VEC ? 0 : j / 4], fabsf(v[i][j]));
             }
         }
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = VEC ? 8 : 16; o > 0; o >>= 1) {
+            m[0] = max_nan(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+            if (!VEC) m[1] = max_nan(m[1], __shfl_xor_sync(0xffffffffu, m[1], o));
+        }
         if (left <= 0) continue;
-        const float sc = (m > 0.f || m != m) ? m / 448.f : 1.f;
-        // y / scale as y (1 / scale): one rounding more, far below half a step of e4m3;
-        // where 1 / scale overflows (a block below 2^-117) y is divided
-        const float inv = 1.0f / sc;
-        const bool tiny = !(inv < 3.0e38f);
-        if ((tid & 15) == 0) a.scale[row * nblk + e / 128] = sc;
         uint32_t b[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
+            const float mk = m[VEC ? 0 : k];
+            const float sc = (mk > 0.f || mk != mk) ? mk / 448.f : 1.f;
+            // y / scale as y (1 / scale): one rounding more, far below half a step of e4m3;
+            // where 1 / scale overflows (a block below 2^-117) y is divided
+            const float inv = 1.0f / sc;
+            const bool tiny = !(inv < 3.0e38f);
+            if (VEC ? k == 0 && (tid & 15) == 0 : (tid & 31) == 0 && 128 * k < left)
+                a.scale[row * nblk + e / 128 + (VEC ? 0 : k)] = sc;
             float q[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) q[j] = tiny ? v[i][4 * k + j] / sc : v[i][4 * k + j] * inv;
@@ -117,7 +130,7 @@ __device__ __forceinline__ void write_row(const Args& a, int64_t row, float (&v)
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (j < left) qp[j] = (uint8_t)(b[j >> 2] >> (8 * (j & 3)));
+                if (32 * j < left) qp[32 * j] = (uint8_t)(b[j >> 2] >> (8 * (j & 3)));
         }
     }
 }
@@ -148,7 +161,7 @@ __global__ void __launch_bounds__(U == 4 ? 512 : 1024) rmsnorm_kernel(const Args
         T* rp = static_cast<T*>(a.r) + row * a.rs;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int e = 8 * (tid + i * nt);
+            const int e = first<VEC>(i, tid, nt);
             if (e < D) {
                 load8<T, VEC>(xp + e, D - e, v[i]);
             } else {
@@ -160,12 +173,12 @@ __global__ void __launch_bounds__(U == 4 ? 512 : 1024) rmsnorm_kernel(const Args
             float t[U][8];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const int e = 8 * (tid + i * nt);
+                const int e = first<VEC>(i, tid, nt);
                 if (e < D) load8<T, VEC>(rp + e, D - e, t[i]);
             }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const int e = 8 * (tid + i * nt);
+                const int e = first<VEC>(i, tid, nt);
                 if (e < D) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[i][j] += t[i][j];
@@ -186,6 +199,52 @@ __global__ void __launch_bounds__(U == 4 ? 512 : 1024) rmsnorm_kernel(const Args
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         write_row<U, VEC>(a, row, v, 1.0f / sqrtf(sum / (float)D + a.eps), tid, nt);
+    }
+}
+
+// Many narrow rows: a row a warp, so no barriers and no thread without a unit but the last.
+template <typename T, int U>
+__global__ void __launch_bounds__(256) rmsnorm_warp_kernel(const Args a) {
+    const int D = a.D, lane = threadIdx.x & 31;
+    for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < a.rows; row += (int64_t)gridDim.x * 8) {
+        float v[U][8];
+        const T* xp = static_cast<const T*>(a.x) + row * a.xs;
+        T* rp = static_cast<T*>(a.r) + row * a.rs;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int e = 8 * (lane + 32 * i);
+            if (e < D) {
+                load8<T, true>(xp + e, D - e, v[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+            }
+        }
+        if (a.r) {
+            float t[U][8];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int e = 8 * (lane + 32 * i);
+                if (e < D) load8<T, true>(rp + e, D - e, t[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int e = 8 * (lane + 32 * i);
+                if (e < D) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i][j] += t[i][j];
+                    store8<T, true>(rp + e, D - e, v[i]);
+                }
+            }
+        }
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        write_row<U, true>(a, row, v, 1.0f / sqrtf(ss / (float)D + a.eps), lane, 32);
     }
 }
 

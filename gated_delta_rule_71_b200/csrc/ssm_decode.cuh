@@ -17,7 +17,7 @@
 // owns 64 state columns (32 at P = 32): warp w holds the rows [w*N/8, (w+1)*N/8),
 // lane l two columns, so each row is one coalesced 256-byte access, loaded and
 // stored with streaming hints (touched once a step).  256 requests, H 32, G 16, P = N =
-// 128: 190 us, 5.8 TB/s (88 % of a copy's rate, the convolution's launch included); one
+// 128: 187 us, 5.9 TB/s (90 % of a copy's rate, the convolution's launch included); one
 // request, H 32, P 64, N 128: 4.2 us, two launches' latency.
 #pragma once
 
@@ -74,6 +74,62 @@ __global__ void __launch_bounds__(128) decode_conv_kernel(const DecodeArgs a) {
         a.v[(int64_t)r * a.C + c] = a.act ? silu_f32(acc) : acc;
 #pragma unroll
         for (int i = 0; i + 1 < W; ++i) win[i] = t[i + 1];
+    }
+}
+
+// The same for rows, windows and taps on 16 bytes (C is a multiple of 32): eight channels a thread,
+// so a window is W - 1 loads of 16 bytes, and the windows of four requests are in flight.
+// Grid: x over units of eight channels (128 per block), y over runs of kDecVecReqs requests.
+constexpr int kDecVecReqs = 4;
+template <int W>
+__global__ void __launch_bounds__(128) decode_conv_vec_kernel(const DecodeArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int c = 8 * (blockIdx.x * 128 + threadIdx.x);
+    if (c >= a.C) return;
+    const int r0 = blockIdx.y * kDecVecReqs;
+    uint4 win[kDecVecReqs][W > 1 ? W - 1 : 1], in[kDecVecReqs];
+    int64_t at[kDecVecReqs];  // of the window, or -1
+#pragma unroll
+    for (int k = 0; k < kDecVecReqs; ++k) {
+        const int r = r0 + k, slot = r < a.n ? (a.idx ? a.idx[r] : r) : -1;
+        at[k] = slot < 0 || slot >= a.n_slots ? -1 : ((int64_t)slot * a.C + c) * (W - 1);
+        if (at[k] < 0) continue;
+        in[k] = *reinterpret_cast<const uint4*>(a.row + (int64_t)r * a.rs + c);
+#pragma unroll
+        for (int i = 0; i + 1 < W; ++i) win[k][i] = reinterpret_cast<const uint4*>(a.cstate + at[k])[i];
+    }
+    float4 wv[2 * W];
+    float b[8];
+    const float* w = reinterpret_cast<const float*>(wv);
+#pragma unroll
+    for (int i = 0; i < 2 * W; ++i) wv[i] = reinterpret_cast<const float4*>(a.w + (int64_t)c * W)[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = a.bias ? a.bias[c + i] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kDecVecReqs; ++k) {
+        if (at[k] < 0) continue;
+        const __nv_bfloat16* t = reinterpret_cast<const __nv_bfloat16*>(win[k]);
+        const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(&in[k]);
+        uint4 next[W > 1 ? W - 1 : 1];
+        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(next);
+        float4 v[2];
+        float* vf = reinterpret_cast<float*>(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float acc = b[j];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const __nv_bfloat16 e = i + 1 < W ? t[j * (W - 1) + i] : x[j];
+                acc = fmaf(w[j * W + i], __bfloat162float(e), acc);
+                if (i > 0) o[j * (W - 1) + i - 1] = e;
+            }
+            vf[j] = a.act ? silu_f32(acc) : acc;
+        }
+        float4* vo = reinterpret_cast<float4*>(a.v + (int64_t)(r0 + k) * a.C + c);
+        vo[0] = v[0];
+        vo[1] = v[1];
+#pragma unroll
+        for (int i = 0; i + 1 < W; ++i) reinterpret_cast<uint4*>(a.cstate + at[k])[i] = next[i];
     }
 }
 
