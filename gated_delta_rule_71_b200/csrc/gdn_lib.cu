@@ -762,8 +762,13 @@ gdn_status gdn_ssm_scan(const void* x, int64_t x_stride, const void* dt, int64_t
     cudaStream_t st = as_stream(stream);
     if (dtype == GDN_F32) return launch_scan_simt<float>(a, st);
     using gdn::ssm::tma_rows;
-    // rows on 16 bytes (y is [rows, H, P] and needs the same) take the tensor cores
-    if (rows > 0 && rows < ((int64_t)1 << 31) && tma_rows(x, x_stride) && tma_rows(Bm, b_stride) &&
+    // Few tokens walk faster than a chunk is set up, and every rounding there is fp32's (one
+    // sequence, H 32, P 64, N 128: 1 token 8.2 us against 16.4, 32 16.0 against 16.9, 48 25.0
+    // against 17.2), while they do not queue for SMs (64 sequences of 8 tokens, 4096 blocks: 155 us
+    // against 132).  T is a packed batch's total.
+    const bool walk = T <= 32 && (int64_t)n_seq * H * (P / 32) <= 4 * (int64_t)num_sms();
+    // Rows on 16 bytes (y is [rows, H, P] and needs the same) take the tensor cores.
+    if (!walk && rows > 0 && rows < ((int64_t)1 << 31) && tma_rows(x, x_stride) && tma_rows(Bm, b_stride) &&
         tma_rows(Cm, c_stride) && (!z || tma_rows(z, z_stride)) && aligned16(y) && r.segments * r.units < 0x7fffffff &&
         (r.slots == 0 || (n_seq <= 65535 && r.units <= 65535)))
         return cuda_check(gdn::ssm::launch_scan_tc(a, rows, r, workspace, st));

@@ -4,8 +4,8 @@
 //     dt_t = softplus(dt_raw_t + dt_bias)      a_t = exp(-exp(A_log) dt_t)
 //     h_t  = a_t h_{t-1} + dt_t B_t x_t^T      h [N, P] fp32, key-major
 //     y_t  = (h_t^T C_t + D x_t) silu(z_t)     D and z optional
-// This kernel serves fp32 inputs and rows that TMA cannot address; aligned bf16
-// rows run on the chunked tensor-core kernel (ssm_scan_tc.cuh).
+// This kernel serves fp32 inputs, rows that TMA cannot address and a few tokens;
+// other bf16 rows run on the chunked tensor-core kernel (ssm_scan_tc.cuh).
 //
 // Columns p of the state never interact, so a block owns 32 of them: thread
 // (p, s) = (tid / 4, tid % 4) keeps the rows n = 16 j + 4 s + i (i < 4) of
