@@ -13,7 +13,8 @@
 //   S  += (w x)^T B                 S = h^T accumulates in tensor memory in fp32
 // The weights e^{R_s} dt_s are fp32, so w x is split into three bf16 terms (24
 // bits): states keep fp32 accuracy.  W and the copy of h that multiplies C are
-// rounded to bf16 once each, as y itself is.
+// rounded to bf16 once each, as y itself is; where a segment is one chunk (short sequences,
+// whose y is mostly the entering state's) that copy has a second term.
 //
 // Decays are factored so that every exponent is <= 0 (nothing overflows) and is a
 // sum of same-signed terms or a difference within 32 tokens: for s in an earlier
@@ -589,6 +590,17 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                         tc::st_shared_v4(at + tc::sw128_off(ln, (n0 / 8 + i) & 7), tc::pack_bf16(v[8 * i], v[8 * i + 1]),
                                          tc::pack_bf16(v[8 * i + 2], v[8 * i + 3]), tc::pack_bf16(v[8 * i + 4], v[8 * i + 5]),
                                          tc::pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+                    if (nch == 1) {  // what the rounding left, into a tile of x that one chunk leaves free
+                        auto rest = [&](int k) {
+                            const uint32_t w = tc::pack_bf16(v[k], v[k + 1]);
+                            return tc::pack_bf16(v[k] - bf16_lo(w), v[k + 1] - bf16_hi(w));
+                        };
+                        const uint32_t to = sbase + K::OFF_X + (2 + n0 / 64) * K::TILE;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            tc::st_shared_v4(to + tc::sw128_off(ln, (n0 / 8 + i) & 7), rest(8 * i), rest(8 * i + 2),
+                                             rest(8 * i + 4), rest(8 * i + 6));
+                    }
 #pragma unroll
                     for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i] * e);
                     tc::tmem_st16(lane_base + K::COL_S + n0, u);
@@ -852,6 +864,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                     for (int k = 0; k < NP / 16; ++k) {
                         const uint32_t o = (k >> 2) * (K::TILE / 16) + (k & 3) * 2;
                         tc::mma_bf16(tmem + K::COL_Y, tc::desc(lc + o), tc::desc(lh + o), idCB, k > 0);
+                    }
+                    if (nch == 1) {  // its second term
+                        const uint32_t lr = tc::desc_lo(sbase + K::OFF_X + 2 * K::TILE, 16);
+#pragma unroll 1
+                        for (int k = 0; k < NP / 16; ++k) {
+                            const uint32_t o = (k >> 2) * (K::TILE / 16) + (k & 3) * 2;
+                            tc::mma_bf16(tmem + K::COL_Y, tc::desc(lc + o), tc::desc(lr + o), idCB, 1);
+                        }
                     }
                     tc::mma_commit(&bars[Y_FULL]);
                     tc::mma_commit(&bars[Y_FULL + 1]);
