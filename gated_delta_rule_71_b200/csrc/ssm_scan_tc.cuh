@@ -31,10 +31,11 @@
 // x, B, C and z come in and y goes out by TMA tiles; x^T reaches tensor memory by
 // transposing 8 x 8 loads (ldmatrix.trans, st.16x128b).
 //
-// What bounds it: issue slots.  A chunk takes 5700 to 7000 cycles an SM (with a gate:
-// 7000), 60 to 68 % of the slots used: the warps' work on CB, x, S and y is some 5500
-// warp instructions a scheduler, and the gate's silu fills the special-function units.
-// The products (3300 cycles at N = 128) and HBM (a third of its rate) are below that.
+// What bounds it: the chain of hand-overs in a chunk (CB, W, W x; S, C h, y) with more than
+// half of the issue slots taken by the work beside it.  A chunk takes 5700 to 7000 cycles
+// an SM (with a gate 7000 or more); the warps' work on CB, x, S and y is some 4700 warp
+// instructions a scheduler, the products are 3300 cycles at N = 128 (36 % of the tensor
+// pipe), HBM runs at a third of its rate.
 // Measured: 4 x 4096 tokens, H 32, G 8, P 64, N 128, gate: 117 us; 8 packed sequences of
 // 32768 tokens in all, H 32, G 16, P = N = 128: 385 us; one of 131072, H 32, P = N = 64: 520 us
 // (token by token: 4131, 10462 and 58698 us).  Steps that gave most, on the first: z
