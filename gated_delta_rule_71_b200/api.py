@@ -460,9 +460,19 @@ def _row_stride(t: torch.Tensor, name: str, inner: int) -> int:
 
 
 @functools.lru_cache(maxsize=256)
+def _scan_workspace(index: int, n_seq: int, T_total: int, H: int, G: int, P: int, N: int, dtype: int) -> int:
+    # the plan counts the current device's SMs: ask, and remember, per device
+    with torch.cuda.device(index):
+        return int(_lib.load().gdn_ssm_scan_workspace_size(n_seq, T_total, H, G, P, N, dtype))
+
+
 def ssm_scan_workspace_size(n_seq: int, T_total: int, H: int, G: int, P: int, N: int,
-                            dtype=torch.bfloat16) -> int:
-    return int(_lib.load().gdn_ssm_scan_workspace_size(n_seq, T_total, H, G, P, N, _DT[dtype]))
+                            dtype=torch.bfloat16, device=None) -> int:
+    """Bytes of workspace that ssm_scan needs for these sizes on `device` (the current one)."""
+    index = None if device is None else torch.device(device).index
+    if index is None:
+        index = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    return _scan_workspace(index, n_seq, T_total, H, G, P, N, _DT[dtype])
 
 
 def ssm_scan(x: torch.Tensor, dt: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor,
@@ -515,7 +525,7 @@ def ssm_scan(x: torch.Tensor, dt: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tens
     if out.shape != (B, T, H, P):
         raise ValueError("out must be [B, T, H, P]")
     hT = torch.empty((n_seq, H, N, P), dtype=torch.float32, device=dev) if output_final_state else None
-    need = ssm_scan_workspace_size(n_seq, B * T, H, G, P, N, x.dtype)
+    need = _scan_workspace(dev.index, n_seq, B * T, H, G, P, N, _DT[x.dtype])
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is not None:

@@ -401,7 +401,9 @@ gdn_status gdn_accumulate_f32(float* y, const float* x, int64_t n, void* stream)
  *   hT        : fp32 [n_seq, H, N, P], written; NULL to skip; not h0.
  *   workspace : >= gdn_ssm_scan_workspace_size(...) bytes, 16-byte aligned (NULL
  *               where that is 0); its contents on entry do not matter.  Calls
- *               that may run at the same time need one each.
+ *               that may run at the same time need one each.  The size depends on
+ *               the SMs of the device that is current when it is asked for: ask on
+ *               the device of the call.
  * P, N in {32, 64, 128}.  Sums, decays and states are fp32 in every kernel.
  * Sequences are independent: what one holds, a NaN included, reaches no other.
  * Within a sequence a NaN or infinity in x reaches y of its head in the whole

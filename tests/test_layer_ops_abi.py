@@ -137,3 +137,36 @@ def test_definitions_against_closed_forms():
     ys, st, *_ = layer.ssm_decode_step(row, dt[0, 5:], np.ones((128, 1)), np.zeros((1, 128, 0)), A, b, h5, 2, 1,
                                       32, 32, D=D, activation=False)
     assert np.allclose(ys[0], y[0, 5]) and np.allclose(st[0], hT[0])
+
+
+def test_scan_workspace_is_that_of_the_device(monkeypatch):
+    # the size depends on the device's SMs: it is asked for with the call's device current, and one
+    # device's answer is not given for another
+    now = [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *_):
+            now[0] = self.before
+
+    class Lib:
+        @staticmethod
+        def gdn_ssm_scan_workspace_size(*sizes):
+            return 1000 + now[0]
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(_lib, "load", Lib)
+    sizes = (3, 12345, 6, 3, 64, 64)
+    assert gdn.ssm_scan_workspace_size(*sizes) == 1000
+    now[0] = 1
+    assert gdn.ssm_scan_workspace_size(*sizes) == 1001
+    assert gdn.ssm_scan_workspace_size(*sizes, device="cuda:0") == 1000 and now[0] == 1
+    assert gdn.ssm_scan_workspace_size(*sizes, device=torch.device("cuda", 2)) == 1002
+    gdn.api._scan_workspace.cache_clear()
