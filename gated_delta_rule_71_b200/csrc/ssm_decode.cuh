@@ -146,6 +146,9 @@ __global__ void __launch_bounds__(256, 5) decode_state_kernel(const DecodeArgs a
     const int slot = a.idx ? a.idx[r] : r;
     if (slot < 0 || slot >= a.n_slots) {  // padding (uniform across the block)
         if (slot >= a.n_slots && threadIdx.x == 0) record_status(GDN_ERR_INVALID_ARG);
+        // A grid whose blocks are all padding would else be done before the convolution, and what
+        // comes next in the stream could change the slots under it.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         if (threadIdx.x < PB) y[threadIdx.x] = __float2bfloat16_rn(0.f);
         return;
     }

@@ -187,3 +187,19 @@ def test_two_calls_at_once(cuda_device):
     for k, d in enumerate(sets):
         assert all(torch.equal(a, b) for a, b in zip(got[k], refs[k]["y"]))
         assert torch.equal(d["state"], refs[k]["state"]) and torch.equal(d["conv_state"], refs[k]["conv_state"])
+
+
+@pytest.mark.parametrize("n", [5, 200])
+def test_a_batch_of_padding_is_done_when_its_call_is(cuda_device, n):
+    # what comes next in the stream may name live slots in the same tensor: none of them is touched
+    d = make(n, n, 2, 1, 64, 64, seed=31)
+    idx = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    live = torch.arange(n, dtype=torch.int32, device="cuda")
+    before = clone(d)
+    for _ in range(50):
+        y = gdn.ssm_decode_step(**d, state_indices=idx)
+        idx.copy_(live)
+        assert not y.any()
+        idx.fill_(-1)
+    assert torch.equal(d["state"], before["state"]) and torch.equal(d["conv_state"], before["conv_state"])
+    assert gdn.device_status() == 0
