@@ -110,7 +110,8 @@ __device__ __forceinline__ void write_row(const Args& a, int64_t row, float (&v)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const float mk = m[VEC ? 0 : k];
-            const float sc = (mk > 0.f || mk != mk) ? mk / 448.f : 1.f;
+            const float mx = mk / 448.f;
+            const float sc = (mx > 0.f || mx != mx) ? mx : 1.f;  // 0: no value of the block is above 2^-141
             // y / scale as y (1 / scale): one rounding more, far below half a step of e4m3;
             // where 1 / scale overflows (a block below 2^-117) y is divided
             const float inv = 1.0f / sc;

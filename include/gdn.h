@@ -460,7 +460,8 @@ gdn_status gdn_ssm_decode_step(const void* row, int64_t row_stride, const void* 
  * addition, a root-mean-square norm, and an output in e4m3 with one fp32 scale
  * per row and block of 128 elements (the operand of gdn_fp8_matmul).
  *     s = x + residual, residual <- s (rounded to dtype);  y = s rsqrt(mean s^2 + eps) w
- *     scale = max|y| / 448 over the block (1 for a block of zeros);  q = e4m3(y / scale)
+ *     scale = max|y| / 448 over the block (1 where that is 0 in fp32: a block of
+ *     zeros, or of nothing above 2^-141);  q = e4m3(y / scale)
  * s and y are fp32; the norm is of the unrounded sum.  The last block of a row
  * may be shorter.  A NaN or infinity in a row makes that row's scales and values
  * NaN where it reaches them, and no other row's.

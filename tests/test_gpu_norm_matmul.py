@@ -300,3 +300,17 @@ def test_offsets_behind_two_to_the_31(cuda_device):
     torch.cuda.synchronize()
     assert gdn.device_status() == 0
     check_matmul((a[-40:], sa[-40:], w, sw), out[-40:])
+
+
+@pytest.mark.parametrize("rows,D", [(1, 300), (1, 296), (1300, 256), (1300, 1024)])
+def test_norm_of_values_whose_scale_underflows(cuda_device, rows, D):
+    # y near 2^-143: max|y| / 448 is 0 in fp32, so the scale is 1 and the values round to 0
+    x = torch.ones(rows, D, device="cuda")
+    x[:, 1::2] = 0.0
+    q, sc = gdn.rmsnorm_fp8(x, torch.full((D,), 1e-43, device="cuda"))
+    assert (sc == 1).all() and not q.float().any()
+    # at 448 units of the smallest fp32 number the scale is that number, and the values are exact
+    w = torch.full((D,), 448 * 2.0 ** -149, device="cuda")
+    x[:] = 1.0
+    q, sc = gdn.rmsnorm_fp8(x, w, eps=0.0)
+    assert (sc == 2.0 ** -149).all() and (q.float() == 448).all()
