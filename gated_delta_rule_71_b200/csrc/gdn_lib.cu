@@ -684,20 +684,19 @@ gdn_status rmsnorm_sized(const gdn::nrm::Args& a, cudaStream_t st) {
         gdn_status s = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
         if (s != GDN_OK) return s;
         const int per = (int)(200 * 1024 / smem) < 8 ? (int)(200 * 1024 / smem) : 8;
-        const int64_t blocks = (int64_t)num_sms() * (per < 1 ? 1 : per);
+        const int64_t blocks = (int64_t)num_sms() * per;
         kern<<<(unsigned)(a.rows < blocks ? a.rows : blocks), 256, smem, st>>>(a);
         return launch_check();
     }
     // The register form: two units a thread for many rows (16384 x 4096 bf16: one 146 us,
-    // two 109, four 161), one for few rows, where latency counts.
+    // two 109, four 161) and for rows that 1024 threads of one do not cover, one for few rows,
+    // where latency counts; eight beyond 1024 threads of two (D above 16384), whose values spill
+    // in 64 registers a thread (bf16 with a residual: 4096 x 16384 137 us, 2048 x 32768 235).
     const int units = (a.D + 7) / 8;
-    int u = a.rows >= 2 * num_sms() ? 2 : 1;
-    while (u < 8 && units > (u == 4 ? 512 : 1024) * u) u *= 2;
-    while (u > 1 && units <= 32 * (u / 2)) u /= 2;
+    const int u = units > 2048 ? 8 : units > 1024 || (a.rows >= 2 * num_sms() && units > 32) ? 2 : 1;
     const int nt = ((units + u - 1) / u + 31) / 32 * 32;
     if (u == 1) return launch_rmsnorm<T, 1, VEC>(a, nt, st);
     if (u == 2) return launch_rmsnorm<T, 2, VEC>(a, nt, st);
-    if (u == 4) return launch_rmsnorm<T, 4, VEC>(a, nt, st);
     return launch_rmsnorm<T, 8, VEC>(a, nt, st);
 }
 

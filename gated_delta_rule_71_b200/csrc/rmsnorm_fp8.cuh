@@ -152,7 +152,7 @@ __device__ __forceinline__ void lds8(const T* p, float (&v)[8]) {
 // keep a later load behind an earlier store), and the sums of two rows alternate between
 // two buffers, so a row costs one barrier.
 template <typename T, int U, bool VEC>
-__global__ void __launch_bounds__(U == 4 ? 512 : 1024) rmsnorm_kernel(const Args a) {
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(const Args a) {
     __shared__ float part[2][32];
     const int D = a.D, nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int flip = 0;
