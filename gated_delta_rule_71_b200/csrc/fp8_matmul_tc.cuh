@@ -30,7 +30,7 @@
 //    shared memory: 245), accumulators in halves of 128 columns 245 (whole: 232).
 //  * 77 x 6176 x 2064: 11.1 us, 1 x 8192 x 4096: 8.4 us, 64 x 8192 x 4096: 11.8 us: launch, the
 //    ring's first fill and the cluster's barriers, then w's bytes at the rate that two CTAs
-//    an SM sustain (one an SM, 17.7 us for the last).
+//    an SM sustain (one an SM, 17.7 us for the last).  1 x 65536 x 4096: 44 us, 6.1 TB/s.
 #pragma once
 
 #include "chunk_tc.cuh"
@@ -443,7 +443,10 @@ inline cudaError_t launch_tc(const Args& g, int split, int sms, cudaStream_t st)
     cfg.blockDim = dim3(C::THREADS, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;
-    cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : (tiles < sms ? tiles : sms)), 1, 1);
+    // Every tile its cluster, or as many CTAs as fit at once, walking the tiles (the small forms two
+    // an SM: 1 x 65536 x 4096 44 us, 64 x 20000 x 4096 22; with one an SM 50 and 32).
+    const int64_t most = (int64_t)C::PER_SM * sms;
+    cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : (tiles < most ? tiles : most)), 1, 1);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)split;

@@ -314,3 +314,19 @@ def test_norm_of_values_whose_scale_underflows(cuda_device, rows, D):
     x[:] = 1.0
     q, sc = gdn.rmsnorm_fp8(x, w, eps=0.0)
     assert (sc == 2.0 ** -149).all() and (q.float() == 448).all()
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,K", [(20000, 384), (40001, 256), (75777, 400)])
+@pytest.mark.parametrize("M", [1, 17, 64, 100])
+def test_matmul_of_few_tokens_onto_a_wide_result(cuda_device, M, N, K, out):
+    # more tiles of 128 weight rows than SMs, and more than CTAs that fit: one CTA walks several, over odd
+    # and even numbers of K blocks
+    ops = operands(M, N, K, M + N + K)
+    buf = torch.full((M + 2, N), 9.0, dtype=out, device="cuda")
+    r = gdn.fp8_matmul(*ops, out_dtype=out, out=buf[1:M + 1])
+    torch.cuda.synchronize()
+    assert gdn.device_status() == 0
+    check_matmul(ops, r)
+    assert (buf[0] == 9).all() and (buf[M + 1] == 9).all()
+    assert torch.equal(r, gdn.fp8_matmul(*ops, out_dtype=out))
