@@ -764,11 +764,12 @@ gdn_status gdn_ssm_scan(const void* x, int64_t x_stride, const void* dt, int64_t
     // Few tokens walk faster than a chunk is set up, and every rounding there is fp32's (one
     // sequence, H 32, P 64, N 128: 1 token 8.2 us against 16.4, 32 16.0 against 16.9, 48 25.0
     // against 17.2), while they do not queue for SMs (64 sequences of 8 tokens, 4096 blocks: 155 us
-    // against 132).  T is a packed batch's total, so many short sequences may pass 32: 36 tokens
-    // in 13 (H 4, P 32, N 128) 9.7 us against 15.8, 109 in 13 14.7 against 16.1, 128 in 13 20.1
-    // against 16.1; one long sequence among them, 128 tokens at the most, 54 against 15.
-    const bool walk = (T <= 32 || (cu_seqlens && T <= 128 && T <= 9 * (int64_t)n_seq)) &&
-                      (int64_t)n_seq * H * (P / 32) <= 4 * (int64_t)num_sms();
+    // against 132).  T is a packed batch's total, and all that is known here of its longest
+    // sequence: with more tokens than 32 in all, few heads' short sequences would still be faster
+    // walked (H 4, P 32, N 128: 36 tokens in 12 7.9 us against 16.8), many heads' no longer
+    // (H 16, P 64, N 128: 104 in 13 19.9 against 17.4), and one long one among them much slower
+    // (14 of one token and one of 100 53 against 19; 12 and one of 105 at H 4, P 32 47 against 19).
+    const bool walk = T <= 32 && (int64_t)n_seq * H * (P / 32) <= 4 * (int64_t)num_sms();
     // Rows on 16 bytes (y is [rows, H, P] and needs the same) take the tensor cores.
     if (!walk && rows > 0 && rows < ((int64_t)1 << 31) && tma_rows(x, x_stride) && tma_rows(Bm, b_stride) &&
         tma_rows(Cm, c_stride) && (!z || tma_rows(z, z_stride)) && aligned16(y) && r.segments * r.units < 0x7fffffff &&

@@ -242,3 +242,19 @@ def test_rows_behind_two_to_the_31(cuda_device):
     assert gdn.device_status() == 0
     assert torch.equal(y[:, T - 300:], y1) and torch.equal(hT[1:], h1)
     check(d, y1, h1)
+
+
+@pytest.mark.parametrize("lens", [[1] * 14 + [100], [8] * 13, [0, 3, 2, 5, 1, 4, 3, 0, 6, 2, 5, 1, 4]])
+def test_a_prompt_packed_with_short_sequences(cuda_device, lens):
+    # a prompt's result does not depend on what it is packed with, and it is not walked token by token
+    T = sum(lens)
+    d = make(1, T, 16, 2, 64, 64, torch.bfloat16, 47, lens)
+    y, hT = gdn.ssm_scan(**d)
+    torch.cuda.synchronize()
+    assert gdn.device_status() == 0
+    check(d, y, hT)
+    n = lens[-1]
+    if n > 32:
+        alone = {k: v[:, T - n:] if k in ("x", "Bm", "Cm", "dt", "z") else v for k, v in d.items()}
+        y1, h1 = gdn.ssm_scan(**{**alone, "h0": d["h0"][-1:], "cu_seqlens": None})
+        assert torch.equal(y[:, T - n:], y1) and torch.equal(hT[-1:], h1)
