@@ -203,3 +203,42 @@ def test_a_batch_of_padding_is_done_when_its_call_is(cuda_device, n):
         idx.fill_(-1)
     assert torch.equal(d["state"], before["state"]) and torch.equal(d["conv_state"], before["conv_state"])
     assert gdn.device_status() == 0
+
+
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("W", [1, 2, 3, 4])
+@pytest.mark.parametrize("n", [64, 67, 130])
+def test_a_decode_batch(cuda_device, n, W, bias):
+    # from 64 requests the convolution takes 16-byte accesses, where rows start on 16 bytes: against the
+    # definition, and bit for bit what it is on rows that do not (the taps add up in the same order)
+    slots = n + 9
+    d = make(n, slots, 4, 2, 32, 32, W, seed=n + W, bias=bias, wide=4)
+    assert d["row"].data_ptr() % 16 == 0 and d["row"].stride(0) % 8 == 0
+    idx = torch.randperm(slots, generator=torch.Generator().manual_seed(n))[:n].to(torch.int32)
+    idx[[0, 5, n - 2]] = -1
+    idx[[9, n - 1]] = torch.tensor([slots, 1 << 30], dtype=torch.int32)
+    d["state_indices"] = idx.cuda()
+    before = clone(d)
+    d["y"] = gdn.ssm_decode_step(**d)
+    assert gdn.device_status() == 1 and gdn.device_status() == 0
+    assert not d["y"][[0, 5, 9, n - 2, n - 1]].any()
+    odd = clone(before)
+    odd["row"] = torch.nn.functional.pad(before["row"], (1, 0))[:, 1:]
+    assert odd["row"].data_ptr() % 16 != 0
+    y = gdn.ssm_decode_step(**odd)
+    assert gdn.device_status() == 1
+    assert torch.equal(y, d["y"]) and torch.equal(odd["state"], d["state"])
+    assert torch.equal(odd["conv_state"], d["conv_state"])
+    before["state_indices"] = torch.where(idx >= slots, -1, idx).cuda()
+    check(d, before)
+
+
+def test_a_decode_batch_without_activation_or_slots(cuda_device):
+    d = make(70, 70, 2, 1, 64, 64, seed=14, wide=6)
+    assert d["row"].data_ptr() % 16 == 0 and d["row"].stride(0) % 8 == 0
+    before = clone(d)
+    y = gdn.ssm_decode_step(**d, activation=False)
+    ry, rs, rc, ym, sm = (torch.from_numpy(t) for t in layer.ssm_decode_step(**before, activation=False))
+    assert ((y.cpu().double() - ry).abs() <= 2.0 ** -8 * ry.abs() + (96 + 64) * E * ym).all()
+    assert ((d["state"].cpu().double() - rs).abs() <= 64 * E * sm).all()
+    assert torch.equal(d["conv_state"].cpu().double(), rc)
