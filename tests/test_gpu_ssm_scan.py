@@ -258,3 +258,20 @@ def test_a_prompt_packed_with_short_sequences(cuda_device, lens):
         alone = {k: v[:, T - n:] if k in ("x", "Bm", "Cm", "dt", "z") else v for k, v in d.items()}
         y1, h1 = gdn.ssm_scan(**{**alone, "h0": d["h0"][-1:], "cu_seqlens": None})
         assert torch.equal(y[:, T - n:], y1) and torch.equal(hT[-1:], h1)
+
+
+@pytest.mark.parametrize("B,T,lens", [(2, 1600, None), (1, 2601, [700, 1, 1500, 0, 400])])
+@pytest.mark.parametrize("h0", [True, False])
+@pytest.mark.parametrize("H,G,P,N", [(6, 2, 64, 128), (4, 2, 128, 128), (3, 1, 128, 64), (10, 2, 32, 32)])
+def test_cut_sequences_of_every_form(cuda_device, H, G, P, N, h0, B, T, lens):
+    # the segments' sums, their chain and the walk from them: one head or two a unit, an odd number of heads
+    # a group (a unit with a missing head), several units, and each width of the state
+    assert gdn.ssm_scan_workspace_size(len(lens or []) or B, B * T, H, G, P, N) > 0
+    d = make(B, T, H, G, P, N, torch.bfloat16, 51, lens, h0=h0)
+    d["A_log"] -= 3.0  # slow decay: what a cut loses would show for long
+    y, hT = gdn.ssm_scan(**d)
+    torch.cuda.synchronize()
+    assert gdn.device_status() == 0
+    check(d, y, hT)
+    y2, hT2 = gdn.ssm_scan(**d)
+    assert torch.equal(y, y2) and torch.equal(hT, hT2)

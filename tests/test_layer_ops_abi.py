@@ -170,3 +170,16 @@ def test_scan_workspace_is_that_of_the_device(monkeypatch):
     assert gdn.ssm_scan_workspace_size(*sizes, device="cuda:0") == 1000 and now[0] == 1
     assert gdn.ssm_scan_workspace_size(*sizes, device=torch.device("cuda", 2)) == 1002
     gdn.api._scan_workspace.cache_clear()
+
+
+def test_scan_workspace_of_a_cut_sequence():
+    one = dict(B=1, T=4600, H=2, G=1, P=64, N=64, xs=128, dts=2, bs=64, cs=64)
+    need = _lib.load().gdn_ssm_scan_workspace_size(1, 4600, 2, 1, 64, 64, 1)
+    assert need > 0
+    for bad in (dict(ws=None), dict(wsb=0), dict(wsb=need - 1), dict(ws=ctypes.c_void_p(520))):
+        assert scan(**one, **bad) == INVALID, bad
+    packed = dict(one, cu=p, n_seq=3, h0=p, hT=q)
+    need = _lib.load().gdn_ssm_scan_workspace_size(3, 4600, 2, 1, 64, 64, 1)
+    assert need > 0
+    for bad in (dict(ws=None), dict(wsb=0), dict(ws=ctypes.c_void_p(520))):
+        assert scan(**packed, **bad) == INVALID, bad
