@@ -464,7 +464,8 @@ gdn_status gdn_ssm_decode_step(const void* row, int64_t row_stride, const void* 
  *     zeros, or of nothing above 2^-141);  q = e4m3(y / scale)
  * s and y are fp32; the norm is of the unrounded sum.  The last block of a row
  * may be shorter.  A NaN or infinity in a row makes that row's scales and values
- * NaN where it reaches them, and no other row's.
+ * NaN where it reaches them, and no other row's.  A row whose sum of squares is
+ * past fp32 (values near 2^64) comes out as zeros under scales of 1.
  *   x        : `dtype` [rows, D], row stride x_stride >= D elements.
  *   residual : `dtype` [rows, D], row stride r_stride, in place; NULL for none;
  *              not x.

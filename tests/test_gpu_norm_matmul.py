@@ -10,7 +10,9 @@ import pytest
 import torch
 
 import gated_delta_rule_71_b200 as gdn
+import oracle
 from oracle import layer
+from tests._util import TOL_BF16, relerr
 
 pytestmark = pytest.mark.gpu
 E = 2.0 ** -24
@@ -330,3 +332,90 @@ def test_matmul_of_few_tokens_onto_a_wide_result(cuda_device, M, N, K, out):
     check_matmul(ops, r)
     assert (buf[0] == 9).all() and (buf[M + 1] == 9).all()
     assert torch.equal(r, gdn.fp8_matmul(*ops, out_dtype=out))
+
+
+@pytest.mark.parametrize("ty", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("res", [True, False])
+@pytest.mark.parametrize("rows,D", [(1300, 256), (5000, 64), (2001, 8), (1185, 264), (1300, 512), (1300, 1000), (1300, 2048),
+                                    (1300, 4264)])
+def test_norm_of_many_rows(cuda_device, rows, D, res, ty):
+    # the forms of many rows, one warp a row and streamed, each width of them: contiguous rows, and rows of a wider tensor
+    g = torch.Generator().manual_seed(D)
+    w = (1 + 0.2 * torch.randn(D, generator=g)).cuda()
+    for width, off in ((D, 0), (D + 24, 8)):
+        base = torch.randn(rows, width, generator=g).to(ty).cuda()
+        rbase = (3 * torch.randn(rows, width, generator=g)).to(ty).cuda() if res else None
+        x, keep = base[:, off:off + D], base.clone()
+        r = rbase[:, off:off + D] if res else None
+        r0, rkeep = (r.clone(), rbase.clone()) if res else (None, None)
+        q, sc = gdn.rmsnorm_fp8(x, w, residual=r)
+        torch.cuda.synchronize()
+        assert gdn.device_status() == 0 and torch.equal(base, keep)
+        check_norm(x, w, r0, q, sc, r)
+        if res:
+            rkeep[:, off:off + D] = rbase[:, off:off + D]
+            assert torch.equal(rbase, rkeep)
+
+
+def test_norm_of_rows_past_fp32(cuda_device):
+    # a row whose sum of squares is past fp32 has no finite norm in it: zeros, under scales of one
+    x = torch.ones(1300, 256, device="cuda")
+    x[[1, 77]] = 1e20
+    w = torch.ones(256, device="cuda")
+    for rows in (3, 1300):
+        q, sc = gdn.rmsnorm_fp8(x[:rows], w)
+        for r in (1, 77):
+            if r < rows:
+                assert not q[r].float().any() and (sc[r] == 1).all()
+        assert (q[[0, 2]].float() == 448).all()
+
+
+def test_norm_residuals_of_two_streams(cuda_device):
+    g = torch.Generator().manual_seed(16)
+    sets = [[torch.randn(rows, D, generator=g).bfloat16().cuda() for _ in range(2)] for rows, D in ((2400, 1024), (3000, 256), (40, 1024))]
+    want = [(x.float() + r.float()).bfloat16() for x, r in sets]
+    live = [[r.clone() for _ in range(5)] for _, r in sets]
+    ones = torch.ones(1024, device="cuda")
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for i in range(5):
+        for k, (x, _) in enumerate(sets):
+            with torch.cuda.stream(streams[k]):
+                gdn.rmsnorm_fp8(x, ones[:x.shape[1]], residual=live[k][i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want[k]) for k in range(len(sets)) for t in live[k])
+
+
+def test_projection_into_the_product_rule(cuda_device):
+    """Norm and projection in front of the library's other recurrence: a prompt through gdp_prefill, then a
+    token through gdp_decode_layer_step, both on slices of the projected rows."""
+    M, H, G, P, N, W, Dm, T = 2, 4, 2, 128, 128, 4, 256, 97
+    vals, C = M * H * P, M * H * P + M * G * N + G * N
+    width = C + 16  # [values | keys | queries | ba and padding to 16 bytes]
+    g = torch.Generator().manual_seed(15)
+    r = lambda *s: torch.randn(s, generator=g)
+    w = (100 * r(width, Dm)).clamp(-448, 448).to(F8).cuda()
+    ws = torch.full((-(-width // 128), 2), 0.01 / 16)
+    ws[vals // 128:C // 128] /= N ** 0.5  # keys and queries of about unit norm
+    ws = ws.cuda()
+    x, res = r(T + 3, Dm).bfloat16().cuda(), r(T + 3, Dm).bfloat16().cuda()
+    A_log, dtb = (torch.rand(H, generator=g) * 2).cuda(), (r(H) - 3).cuda()
+    q, s = gdn.rmsnorm_fp8(x, (1 + 0.1 * r(Dm)).cuda(), residual=res)
+    row = gdn.fp8_matmul(q, s, w, ws)
+    check_matmul((q, s, w, ws), row)
+    xs, ba = row[:, :C], row[:, C:C + M * H + H]
+    o, hT = gdn.gdp_prefill(xs[None, :T], ba[None, :T], A_log, dtb, M, H, G, P, N)
+    c = lambda t: t.cpu()
+    ro, rh = oracle.gdp_prefill(c(xs[None, :T]), c(ba[None, :T]), c(A_log), c(dtb), M, H, G, P, N)
+    assert relerr(o, ro) <= TOL_BF16 and relerr(hT, rh) <= TOL_BF16
+    # three requests' tokens, each on a copy of that state
+    st = hT.expand(3, -1, -1, -1).contiguous()
+    cw, cb, cs = (r(C, W) / 2).cuda(), r(C).cuda(), r(3, C, W - 1).bfloat16().cuda()
+    y, rcs = oracle.conv1d_update(c(xs[T:]), c(cw), c(cs), bias=c(cb), activation=True)
+    ro, rs = oracle.gdp_decode_step_indexed(torch.from_numpy(y).float().bfloat16().reshape(3, 1, C), c(ba[T:]).reshape(3, 1, -1),
+                                            c(A_log), c(dtb), c(st), torch.arange(3, dtype=torch.int32), M, H, G, P, N)
+    out = gdn.gdp_decode_layer_step(xs[T:], ba[T:], cw, cs, A_log, dtb, st, M, H, G, P, N, conv_bias=cb)
+    torch.cuda.synchronize()
+    assert gdn.device_status() == 0
+    assert relerr(out, ro) <= TOL_BF16 and relerr(st, rs) <= TOL_BF16
+    assert torch.equal(cs.cpu().float(), torch.from_numpy(rcs).float())
