@@ -556,7 +556,7 @@ def ssm_decode_step(row: torch.Tensor, dt: torch.Tensor, conv_w: torch.Tensor,
     row [n, H*P + 2*G*N] bf16 ([x | B | C], before the convolution; conv_state [n_slots, C, W-1]
     bf16 updated in place, conv_w [C, W] fp32), then one step of ssm_scan's recurrence on
     state [n_slots,H,N,P] fp32, in place.  dt [n, H], z [n, H*P] bf16; rows may be slices of a
-    wider row.  state_indices int32 [n] names each request's slot (-1: padding, y = 0);
+    wider row.  state_indices int32 [n] names each request's slot (-1: padding, y = 0), no slot twice;
     without it request r owns slot r.  Returns y [n,H,P] bf16."""
     _need(row, "row", torch.bfloat16, contiguous=False)
     dev = row.device

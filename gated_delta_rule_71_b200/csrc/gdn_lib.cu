@@ -9,7 +9,6 @@
 #include <cstring>
 #include <mutex>
 #include <type_traits>
-#include <type_traits>
 
 #include "gdn.h"
 #include "common.cuh"

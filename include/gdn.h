@@ -404,10 +404,18 @@ gdn_status gdn_accumulate_f32(float* y, const float* x, int64_t n, void* stream)
  *               that may run at the same time need one each.  The size depends on
  *               the SMs of the device that is current when it is asked for: ask on
  *               the device of the call.
- * P, N in {32, 64, 128}.  Sums, decays and states are fp32 in every kernel.
+ * P, N in {32, 64, 128}.  Sums and states, hT among them, are fp32 in every
+ * kernel.  fp32 rows, bf16 rows that do not start on 16 bytes, and few bf16 tokens
+ * (at most 32 of all packed sequences, or of each of a few dense ones) are walked in
+ * fp32 throughout, and y is rounded once.  Other bf16 rows run in blocks of 128 tokens,
+ * and there two factors of y's products are rounded to bf16 before them: a pair's
+ * weight (Cm_r . Bm_s) dt_s times its decay, with D added to that of a token with
+ * itself, and the state that enters the block (in two bf16 terms where a sequence,
+ * or a part of a long one, is a single block).
  * Sequences are independent: what one holds, a NaN included, reaches no other.
  * Within a sequence a NaN or infinity in x reaches y of its head in the whole
- * block of 128 tokens that holds it (bf16 rows run in blocks), and all later ones.
+ * block of 128 tokens that holds it, the ones before it included, and all later
+ * ones; in blocks an infinity in x or Bm may come out as a NaN, in y and in hT.
  * Errors: INVALID_ARG (NULL or misaligned pointers, sizes < 0, H % G != 0, a
  * stride shorter than a row, B != 1 with cu_seqlens, a short workspace),
  * UNSUPPORTED (other P or N).  As in gdn_chunk_fwd, offsets outside [0, T] are
@@ -462,10 +470,13 @@ gdn_status gdn_ssm_decode_step(const void* row, int64_t row_stride, const void* 
  *     s = x + residual, residual <- s (rounded to dtype);  y = s rsqrt(mean s^2 + eps) w
  *     scale = max|y| / 448 over the block (1 where that is 0 in fp32: a block of
  *     zeros, or of nothing above 2^-141);  q = e4m3(y / scale)
- * s and y are fp32; the norm is of the unrounded sum.  The last block of a row
- * may be shorter.  A NaN or infinity in a row makes that row's scales and values
- * NaN where it reaches them, and no other row's.  A row whose sum of squares is
- * past fp32 (values near 2^64) comes out as zeros under scales of 1.
+ * s and y are fp32; the norm is of the unrounded sum.  y / scale is taken as
+ * y (1 / scale) in fp32, so a value next to the border of two e4m3 numbers may
+ * become either.  The last block of a row may be shorter.  A NaN or infinity in a
+ * row makes that row's scales and values NaN where it reaches them, and no other
+ * row's.  The sum of squares is fp32 too: a row that passes it (values near 2^64)
+ * comes out as zeros under scales of 1, and one that vanishes in it, with eps = 0,
+ * without finite scales.
  *   x        : `dtype` [rows, D], row stride x_stride >= D elements.
  *   residual : `dtype` [rows, D], row stride r_stride, in place; NULL for none;
  *              not x.
@@ -487,8 +498,9 @@ gdn_status gdn_rmsnorm_fp8(const void* x, int64_t x_stride, void* residual, int6
  *   w : e4m3 bytes [N, K], row stride w_stride >= K;
  *       w_scales fp32 [ceil(N/128), ceil(K/128)].
  *   out : [M, N] of out_dtype (GDN_F32 or GDN_BF16), contiguous; overlaps no input.
- * The two scales are multiplied first, in fp32.  M == 0 is a no-op.  Operands whose rows start on 16 bytes run on the tensor
- * cores; others on a plain fp32 kernel, much slower.
+ * The two scales are multiplied first, in fp32.  M == 0 is a no-op.  Operands whose
+ * rows start on 16 bytes run on the tensor cores; others on a plain fp32 kernel,
+ * much slower.
  * Errors: INVALID_ARG (NULL or misaligned pointers, sizes, strides), UNSUPPORTED
  * (M > 64 * 65535, N or K > 2^30).
  */

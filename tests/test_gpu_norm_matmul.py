@@ -419,3 +419,13 @@ def test_projection_into_the_product_rule(cuda_device):
     assert gdn.device_status() == 0
     assert relerr(out, ro) <= TOL_BF16 and relerr(st, rs) <= TOL_BF16
     assert torch.equal(cs.cpu().float(), torch.from_numpy(rcs).float())
+
+
+def test_norm_of_rows_that_vanish_in_fp32(cuda_device):
+    # with eps = 0 a row whose squares are 0 in fp32 has no finite scale; the smallest eps gives it one
+    x = torch.ones(3, 256, device="cuda")
+    x[1] = 1e-30
+    w = torch.ones(256, device="cuda")
+    q, sc = gdn.rmsnorm_fp8(x, w, eps=0.0)
+    assert not sc[1].isfinite().any() and (sc[[0, 2]] == sc[0, 0]).all() and (q[[0, 2]].float() == 448).all()
+    check_norm(x, w, None, *gdn.rmsnorm_fp8(x, w, eps=1e-30), None, eps=1e-30)
