@@ -19,16 +19,18 @@
 // while the last one is written out.
 //
 // What bounds it and what it measured.
-//  * 4096 x 14336 x 4096, bf16 out: 225 us, 2.14 PFLOP/s.  A K block takes about 960 cycles
-//    an SM, of which the products are 522 (4 x 131); reading 128 x 256 sums from tensor
-//    memory and adding them some 500 beside waits; the two overlap by half, since only two
-//    256-column accumulators fit in tensor memory.  1792 tiles are 12.1 rounds of 148 SMs,
-//    taken as 13.  The promotion warps have 168 registers for 128 sums and 32 loaded
+//  * 4096 x 14336 x 4096, bf16 out: 230 us (2.1 PFLOP/s) with the operands in L2, 255 to 270
+//    (1.8) with other ones each time; the power cap holds the clock at 1.5 to 1.6 GHz.  A K
+//    block takes about 900 cycles an SM, of which the products are 522 (4 x 131; the tensor
+//    pipe is 60 % busy) and reading 128 x 256 sums from tensor memory and adding them some
+//    500.  The two accumulators would let those overlap whole; what the rest of the 900 waits
+//    for is not known (issue slots 41 %, L2 47 %, HBM 8 %).  1792 tiles are 12.1 rounds of 148
+//    SMs, taken as 13.  The promotion warps have 168 registers for 128 sums and 32 loaded
 //    ones (ten warps are three on some scheduler), so a few more live values cost a tenth.
 //    Tried: 16 promotion warps of 64 columns 318 us (8 of 128: 292), an accumulator's
 //    loads not ahead of its sums 292 (ahead: 267), rows written a thread each 267 (through
 //    shared memory: 245), accumulators in halves of 128 columns 245 (whole: 232).
-//  * 77 x 6176 x 2064: 11.1 us, 1 x 8192 x 4096: 8.4 us, 64 x 8192 x 4096: 11.8 us: launch, the
+//  * 77 x 6176 x 2064: 11.2 us, 1 x 8192 x 4096: 8.3 us (10.0 with w from HBM), 64 x 8192 x 4096: 11.8 us: launch, the
 //    ring's first fill and the cluster's barriers, then w's bytes at the rate that two CTAs
 //    an SM sustain (one an SM, 17.7 us for the last).  1 x 65536 x 4096: 44 us, 6.1 TB/s.
 #pragma once

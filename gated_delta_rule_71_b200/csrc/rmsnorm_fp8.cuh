@@ -13,9 +13,9 @@
 // registers (few rows, any alignment and width), rows streamed through shared memory
 // (many rows), and a row a warp (many narrow rows).
 //
-// Many rows are bound by HBM: 16384 x 4096 bf16 with a residual, 87 us, 5.4 TB/s (83 %
+// Many rows are bound by HBM: 16384 x 4096 bf16 with a residual, 84 us, 5.6 TB/s (85 %
 // of a copy's rate).  Few rows are bound by latency: 32 x 2048 2.6 us, of which an
-// empty launch is most; 1111 x 1000 fp32 3.7 us.
+// empty launch is most; 1111 x 1000 fp32 3.5 us.
 #pragma once
 
 #include <cuda_fp8.h>

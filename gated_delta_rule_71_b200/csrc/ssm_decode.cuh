@@ -17,8 +17,8 @@
 // owns 64 state columns (32 at P = 32): warp w holds the rows [w*N/8, (w+1)*N/8),
 // lane l two columns, so each row is one coalesced 256-byte access, loaded and
 // stored with streaming hints (touched once a step).  256 requests, H 32, G 16, P = N =
-// 128: 187 us, 5.9 TB/s (90 % of a copy's rate, the convolution's launch included); one
-// request, H 32, P 64, N 128: 4.2 us, two launches' latency.
+// 128: 183 us, 6.0 TB/s (92 % of a copy's rate, the convolution's launch included); one
+// request, H 32, P 64, N 128: 4.5 us, two launches' latency.
 #pragma once
 
 #include "common.cuh"

@@ -12,9 +12,12 @@
 //                                   memory in place of CB; x as it came
 //   S  += (w x)^T B                 S = h^T accumulates in tensor memory in fp32
 // The weights e^{R_s} dt_s are fp32, so w x is split into three bf16 terms (24
-// bits): states keep fp32 accuracy.  W and the copy of h that multiplies C are
-// rounded to bf16 once each, as y itself is; where a segment is one chunk (short sequences,
-// whose y is mostly the entering state's) that copy has a second term.
+// bits): states keep fp32 accuracy (an infinity does not survive the split: it becomes a
+// NaN).  W and the copy of h that multiplies C are rounded to bf16 once each, since the
+// tensor cores take W x and C h as bf16, as y itself is; where a segment is one chunk (short
+// sequences, whose y is mostly the entering state's) that copy has a second term.  The skip
+// D x rides on W's diagonal and so shares W's rounding: added in fp32 behind the products it
+// would take the Y warps a second reading of x's tile.
 //
 // Decays are factored so that every exponent is <= 0 (nothing overflows) and is a
 // sum of same-signed terms or a difference within 32 tokens: for s in an earlier
@@ -31,13 +34,16 @@
 // x, B, C and z come in and y goes out by TMA tiles; x^T reaches tensor memory by
 // transposing 8 x 8 loads (ldmatrix.trans, st.16x128b).
 //
-// What bounds it: the chain of hand-overs in a chunk (CB, W, W x; S, C h, y) with more than
-// half of the issue slots taken by the work beside it.  A chunk takes 5700 to 7000 cycles
+// What bounds it: the latency of the chain of hand-overs in a chunk (CB, W, W x; S, C h, y), of
+// which a CTA has one in flight; no unit is full.  A chunk takes 5700 to 7000 cycles
 // an SM (with a gate 7000 or more); the warps' work on CB, x, S and y is some 4700 warp
-// instructions a scheduler, the products are 3300 cycles at N = 128 (36 % of the tensor
-// pipe), HBM runs at a third of its rate.
+// instructions a scheduler (56 % of the issue slots), the products are 3300 cycles at N = 128
+// (36 % of the tensor pipe), HBM runs at a third of its rate.  Where P is 64 or 32 and H / G odd,
+// one CTA of a group has half its lanes empty; P = 32 fills half of each half, and N = 32 runs
+// as 64.
 // Measured: 4 x 4096 tokens, H 32, G 8, P 64, N 128, gate: 117 us; 8 packed sequences of
-// 32768 tokens in all, H 32, G 16, P = N = 128: 385 us; one of 131072, H 32, P = N = 64: 520 us
+// 32768 tokens in all, H 32, G 16, P = N = 128: 370 to 410 us; one of 131072, H 32, P = N = 64: 520 us
+// in a short run at 1965 MHz, 590 over seconds, where the power cap holds 1725
 // (token by token: 4131, 10462 and 58698 us).  Steps that gave most, on the first: z
 // and y through tiles, not a row a thread, 197 to 163; x transposed by its loads and two
 // warpgroups on W, 163 to 153; gates on the S warps and two MMA warps, 143 to 135.
