@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(256) rmsnorm_warp_kernel(const Args a) {
 // The same over many rows of moderate width, with the rows streamed through shared memory
 // by bulk copies: a block keeps two rows in flight behind the one it works on, whatever
 // its warps are doing, which the register form cannot (16384 x 4096 bf16 with a residual:
-// 109 us there at its best, 87 here).  Each thread reads its own units from the stage; the barrier
+// 109 us there at its best, 84 here).  Each thread reads its own units from the stage; the barrier
 // of the row's sum is also the one after which the stage is refilled.
 constexpr int kStages = 3;
 template <typename T, int U>
