@@ -10,7 +10,8 @@
 //   Y2  = C h                       h in bf16 from shared memory
 //   Y1  = W x                       W = the decayed, masked CB in bf16, in tensor
 //                                   memory in place of CB; x as it came
-//   S  += (w x)^T B                 S = h^T accumulates in tensor memory in fp32
+//   S  += (w x)^T B                 S = h^T, or where decays are slow what its bf16 copy lacks,
+//                                   accumulates in tensor memory in fp32 (kSlow)
 // The weights e^{R_s} dt_s are fp32, so w x is split into three bf16 terms (24
 // bits): states keep fp32 accuracy (an infinity does not survive the split: it becomes a
 // NaN).  W and the copy of h that multiplies C are rounded to bf16 once each, since the
@@ -28,7 +29,7 @@
 // one head of 128) of one segment of a sequence.  28 warps, each with one job:
 //   X (4)  reads x, writes the split (w x)^T to tensor memory, 32 tokens at a time
 //   M (8)  turns CB into W          S (4)  makes the gates two chunks ahead; decays S,
-//                                          hands its bf16 copy to C h
+//                                          hands its bf16 copy to C h (at N = 128 X takes half)
 //   Y (8)  e^G Y2, then y = Y1 + that (the skip D x rides on W's diagonal), gate
 //   MMA (2): CB, C h, W x; and the state's products   TMA (2): x, B, C; and z, y tiles
 // x, B, C and z come in and y goes out by TMA tiles; x^T reaches tensor memory by
@@ -41,9 +42,9 @@
 // (36 % of the tensor pipe), HBM runs at a third of its rate.  Where P is 64 or 32 and H / G odd,
 // one CTA of a group has half its lanes empty; P = 32 fills half of each half, and N = 32 runs
 // as 64.
-// Measured: 4 x 4096 tokens, H 32, G 8, P 64, N 128, gate: 117 us; 8 packed sequences of
-// 32768 tokens in all, H 32, G 16, P = N = 128: 370 to 410 us; one of 131072, H 32, P = N = 64: 520 us
-// in a short run at 1965 MHz, 590 over seconds, where the power cap holds 1725
+// Measured: 4 x 4096 tokens, H 32, G 8, P 64, N 128, gate: 121 us; 8 packed sequences of
+// 32768 tokens in all, H 32, G 16, P = N = 128: 380 to 420 us; one of 131072, H 32, P = N = 64: 565 us
+// in short runs, 600 over seconds, where the power cap holds the clock at 1.7 GHz
 // (token by token: 4131, 10462 and 58698 us).  Steps that gave most, on the first: z
 // and y through tiles, not a row a thread, 197 to 163; x transposed by its loads and two
 // warpgroups on W, 163 to 153; gates on the S warps and two MMA warps, 143 to 135.
@@ -62,6 +63,16 @@ namespace ssm {
 constexpr int L = 128;          // tokens of a chunk
 constexpr int kScanThreads = 896;
 constexpr int NGR = 3;          // gate ring
+// A product truncates the sum in tensor memory that it is added to, half a step off it on average and
+// always towards zero, so a chunk's 24 products take some 12 x 2^-24 of a state S that stays there whole.
+// Where a state keeps the share e of itself over a chunk that adds up to 12 / (1 - e): 50 x 2^-24 at 3/4;
+// where nothing decays to 1.2e-5 of S after 32 chunks, 1.3e-4 after 512.  Above 3/4, therefore, S holds only
+// what the bf16 copy of the state lacks, 2^-9 of it, and the copy is added back in fp32 for the next chunk
+// (3.5e-7 after 32 chunks, 8e-6, the rounding of e, after 512).  Slow heads take 8 % longer by it, others none.
+constexpr float kSlow = 0.75f;
+// The first pass has no copy, and no decay between chunks: the sums of kGroup chunks at a time are added up
+// in fp32 in shared memory (37 us for 64 segments of 16 chunks, 35 left in tensor memory; groups of 4: 42).
+constexpr int kGroup = 8;
 constexpr float kMinG2 = -160.f;  // 2^-160 is 0 in fp32: more decay changes nothing
 
 struct Gates {                  // of one chunk and head; sums in log2 units
@@ -92,6 +103,10 @@ struct ScanCfg {
     // (refilled, from L2, under the products that do not need it)
     static constexpr int NBC = NP == 128 ? 1 : 2;
     static constexpr int NXB = NP == 128 ? 5 : 6;       // half-tiles of x
+    // state columns of the S warps; the rest are the X warps', whose buffers are full when the state is
+    // due (slow decays: 94 us of the main pass of 4 x 4096 against 101; at 64 columns the X warps are
+    // the ones waited for, 426 us of one of 131072 against 405)
+    static constexpr int NS = 64;
     static constexpr uint32_t TILE = 16384;             // 128 rows of 128 bytes
     static constexpr uint32_t BT = NH * TILE;
     static constexpr uint32_t OFF_B = 0;                // [NBC]
@@ -102,6 +117,8 @@ struct ScanCfg {
     static constexpr uint32_t OFF_G = OFF_H + BT;       // [NGR][2] Gates
     static constexpr uint32_t OFF_BAR = OFF_G + NGR * 2 * (uint32_t)sizeof(Gates);
     static constexpr uint32_t SMEM = OFF_BAR + 60 * 8 + 16 + 1024;
+    static constexpr uint32_t OFF_SUM = OFF_Z;          // first pass: [NP][128] fp32, over z and h
+    static_assert(OFF_SUM + NP * 512 <= OFF_G, "the sums fit");
     static_assert(SMEM <= 232448, "shared memory budget");
     // tensor memory columns
     static constexpr uint32_t COL_CB = 0;               // fp32 CB, then W of both heads
@@ -110,14 +127,19 @@ struct ScanCfg {
     static constexpr uint32_t COL_WX = COL_Y + 128;     // [2] x 48: three terms of 32 tokens
     static constexpr uint32_t COL_WX1 = COL_Y;          // [4] x 48 in the first pass
     static_assert(COL_WX + 96 <= 512 && COL_WX1 + 192 <= 512, "tensor memory budget");
+    // first pass: two accumulators, of NP columns each
+    static __device__ __forceinline__ uint32_t col_acc(int group) { return group & 1 ? COL_S : COL_CB; }
 };
 
 enum : int {
     B_FULL = 0, B_FREE = B_FULL + 4, C_FULL_ = B_FREE + 4, C_FREE_ = C_FULL_ + 2, X_FULL = C_FREE_ + 2,
     X_DONE = X_FULL + 6, Z_FULL = X_DONE + 6, Y_OUT = Z_FULL + 2, G_FULL = Y_OUT + 2, G_FREE = G_FULL + NGR, CB_FULL = G_FREE + NGR, M_FULL, W_FREE,
     XQ_FULL, XQ_FREE = XQ_FULL + 4, S_READY = XQ_FREE + 4, DS_DONE, H_FREE, Y_FULL, Y_FREE = Y_FULL + 2,
-    CLEAN = Y_FREE + 2, S_DRAIN, N_SCAN_BARS = S_DRAIN + 2
+    CLEAN = Y_FREE + 2, S_DRAIN, N_SCAN_BARS = S_DRAIN + 2,
+    // of the first pass's two accumulators, in place of barriers of what it does not have
+    ACC_FULL = DS_DONE, ACC_FREE = Y_FREE
 };
+static_assert(H_FREE == ACC_FULL + 1, "two barriers of one arrival");
 static_assert(N_SCAN_BARS <= 60, "barrier slots");
 
 // 3-D tiled load of one box (x innermost), completing on `bar`.
@@ -243,6 +265,7 @@ template <int NP, bool STATES, bool ONE>
 __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_constant__ ScanTcArgs p) {
     using K = ScanCfg<NP>;
     constexpr int NH = K::NH, NXB = K::NXB, NBC = K::NBC;
+    constexpr int NS = K::NS;
     constexpr int NB = STATES ? 2 * NBC : NBC;  // the first pass has no C: its room is for B
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -281,7 +304,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             if (i >= G_FULL && i < G_FULL + NGR) n = 4;
             if (i >= G_FREE && i < G_FREE + NGR) n = STATES ? 16 : 20;
             if (i == M_FULL) n = 8;
-            if ((i >= XQ_FULL && i < XQ_FULL + 4) || i == S_READY || i == Y_OUT || i == Y_OUT + 1 || i == Y_FREE ||
+            if (i == S_READY) n = NS < NP ? 8 : 4;
+            if ((i >= XQ_FULL && i < XQ_FULL + 4) || i == Y_OUT || i == Y_OUT + 1 || i == Y_FREE ||
                 i == Y_FREE + 1 || i == CLEAN)
                 n = 4;
             mbar_init(&bars[i], n);
@@ -306,6 +330,130 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     const int q = warp & 3, ln = 32 * q + lane;  // tensor-memory lane of the four-warp jobs
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
 
+    // The state between the chunks, its columns n_lo .. n_hi, by the S warps and (at 128 columns) the X warps.
+    auto enter = [&](int n_lo, int n_hi) {  // the state that enters the segment
+        const Half hf = half(q >> 1);
+        const float* src = nullptr;
+        int64_t step = 0;
+        if ((ln & 63) < hf.width) {
+            if (sg.j > 0) {
+                src = p.part + ((int64_t)(sg.slot + sg.j - 1) * p.units + unit) * a.N * 128 + ln;
+                step = 128;
+            } else if (a.h0) {
+                src = a.h0 + (((int64_t)sg.seq * a.H + hf.head) * a.N) * a.P + hf.col + (ln & 63);
+                step = a.P;
+            }
+            src += n_lo * step;
+        }
+#pragma unroll 1
+        for (int n0 = n_lo; n0 < n_hi; n0 += 16) {
+            uint32_t u[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                u[i] = step && n0 + i < a.N ? __float_as_uint(__ldg(src)) : 0u;
+                src += step;
+            }
+            tc::tmem_st16(lane_base + K::COL_S + n0, u);
+        }
+        tc::tmem_wait_st();
+    };
+    // Sixteen columns of it: S, and e times the last copy where that is not in S (e is 0 where it is).
+    auto state16 = [&](int n0, float e, float (&v)[16]) {
+        tc::tmem_ld16(lane_base + K::COL_S + n0, v);
+        if (e != 0.f) {
+            const uint32_t at = sbase + K::OFF_H + (n0 / 64) * K::TILE;
+            const uint4 h0 = tc::ld_shared_v4(at + tc::sw128_off(ln, (n0 / 8) & 7));
+            const uint4 h1 = tc::ld_shared_v4(at + tc::sw128_off(ln, (n0 / 8 + 1) & 7));
+            const uint32_t w[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 t = __ffma2_rn(make_float2(bf16_lo(w[i]), bf16_hi(w[i])), make_float2(e, e),
+                                            make_float2(v[2 * i], v[2 * i + 1]));
+                v[2 * i] = t.x;
+                v[2 * i + 1] = t.y;
+            }
+        } else {
+            tc::tmem_wait_ld();
+        }
+    };
+    // The state that enters chunk c: its bf16 copy to shared memory, and e times it, or, where the copy
+    // stays apart, e times what the copy lacks, to S.  ep: what this returned for the chunk before.
+    auto advance = [&](int c, int n_lo, int n_hi, float ep) {
+        const float e = gates[2 * (c % NGR) + (ONE ? 0 : q >> 1)].last;
+        const bool apart = e > kSlow || nch == 1;
+        if (c > 0) wait(DS_DONE, c - 1);
+        if (c > 0) wait(H_FREE, c - 1);
+        __syncwarp();
+        tc::tc_after_sync();
+        const uint32_t hrow = sbase + K::OFF_H;
+        if (!apart && ep == 0.f) {  // (a loop of its own: 6 % of the main pass)
+#pragma unroll 1
+            for (int n0 = n_lo; n0 < n_hi; n0 += 16) {
+                float v[16];
+                uint32_t u[16];
+                tc::tmem_ld16(lane_base + K::COL_S + n0, v);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    tc::st_shared_v4(hrow + (n0 / 64) * K::TILE + tc::sw128_off(ln, (n0 / 8 + i) & 7),
+                                     tc::pack_bf16(v[8 * i], v[8 * i + 1]), tc::pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                     tc::pack_bf16(v[8 * i + 4], v[8 * i + 5]), tc::pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+#pragma unroll
+                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i] * e);
+                tc::tmem_st16(lane_base + K::COL_S + n0, u);
+            }
+        } else {
+            const float2 part = apart ? make_float2(-1.f, -1.f) : make_float2(0.f, 0.f);
+#pragma unroll 1
+            for (int n0 = n_lo; n0 < n_hi; n0 += 16) {
+                float v[16];
+                uint32_t u[16];
+                state16(n0, ep, v);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t off = (n0 / 64) * K::TILE + tc::sw128_off(ln, (n0 / 8 + i) & 7);
+                    uint32_t h[4], rest[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int at = 8 * i + 2 * k;
+                        h[k] = tc::pack_bf16(v[at], v[at + 1]);
+                        const float2 t = __ffma2_rn(make_float2(bf16_lo(h[k]), bf16_hi(h[k])), part, make_float2(v[at], v[at + 1]));
+                        rest[k] = tc::pack_bf16(t.x, t.y);
+                        u[at] = __float_as_uint(t.x * e);
+                        u[at + 1] = __float_as_uint(t.y * e);
+                    }
+                    tc::st_shared_v4(hrow + off, h[0], h[1], h[2], h[3]);
+                    if (nch == 1)  // the rest in bf16, into a tile of x that one chunk leaves free
+                        tc::st_shared_v4(sbase + K::OFF_X + 2 * K::TILE + off, rest[0], rest[1], rest[2], rest[3]);
+                }
+                tc::tmem_st16(lane_base + K::COL_S + n0, u);
+            }
+        }
+        tc::tmem_wait_st();
+        tc::fence_async_smem();
+        tc::tc_before_sync();
+        arrive(S_READY);
+        return apart ? e : 0.f;
+    };
+    auto leave = [&](int n_lo, int n_hi, float ep) {  // the state that leaves the sequence
+        if (nch > 0) wait(DS_DONE, nch - 1);
+        __syncwarp();
+        tc::tc_after_sync();
+        const Half hf = half(q >> 1);
+        const bool live = a.hT && sg.j == sg.n - 1 && (ln & 63) < hf.width;
+        float* dst = live ? a.hT + (((int64_t)sg.seq * a.H + hf.head) * a.N + n_lo) * a.P + hf.col + (ln & 63) : nullptr;
+#pragma unroll 1
+        for (int n0 = n_lo; n0 < n_hi; n0 += 16) {
+            float v[16];
+            state16(n0, ep, v);
+            if (live)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (n0 + i < a.N) dst[(int64_t)(n0 - n_lo + i) * a.P] = v[i];
+        }
+    };
+
     if (warp < 4 || (STATES && (warp < 12 || (warp >= 16 && warp < 20)))) {
         // =============================================================== X warps
         // A chunk goes through in quarters of 32 tokens and two buffers of tensor memory
@@ -320,6 +468,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 #pragma unroll
         for (int hb = 0; hb < 2; ++hb)
             off[hb] = (tm >> 1) * 1024 + tr * 128 + (((uint32_t)(4 * (q & 1) + 2 * hb + (tm & 1)) ^ tr) << 4);
+        float ep = 0.f;
+        if constexpr (!STATES && NS < NP) enter(NS, NP);
         for (int c = 0; c < nch; ++c) {
             const int gs = c % NGR, xi = 2 * c + j, xb = xi % NXB;
             if (c == nch - 1 && tail < L) {
@@ -378,10 +528,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 tc::tmem_wait_st();
                 tc::tc_before_sync();
                 arrive(XQ_FULL + buf);
+                // the next buffer is free once the last chunk's state is summed
+                if (!STATES && NS < NP && k == 0) ep = advance(c, NS, NP, ep);
             }
             arrive(X_DONE + xb);
             arrive(G_FREE + gs);
         }
+        if constexpr (!STATES && NS < NP) leave(NS, NP, ep);
     } else if (warp < 12) {
         // =============================================================== M warps
         if constexpr (!STATES) {
@@ -468,33 +621,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         }
     } else if (warp < 16) {
         // =============================================================== S warps
-        const int j = ln >> 6, pc = ln & 63;
-        const Half hf = half(j);
-        const bool live = pc < hf.width;
-        const int64_t hb = (((int64_t)sg.seq * a.H + hf.head) * a.N) * a.P + hf.col + pc;
-        // the state that enters the segment
-        const float* src = nullptr;
-        int64_t step = 0;
-        if (!STATES && live) {
-            if (sg.j > 0) {
-                src = p.part + ((int64_t)(sg.slot + sg.j - 1) * p.units + unit) * a.N * 128 + ln;
-                step = 128;
-            } else if (a.h0) {
-                src = a.h0 + hb;
-                step = a.P;
-            }
-        }
-#pragma unroll 1
-        for (int n0 = 0; n0 < NP; n0 += 16) {
-            uint32_t u[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                u[i] = src && n0 + i < a.N ? __float_as_uint(__ldg(src)) : 0u;
-                src += step;
-            }
-            tc::tmem_st16(lane_base + K::COL_S + n0, u);
-        }
-        tc::tmem_wait_st();
+        if constexpr (!STATES) enter(0, NS);
         // The gates are made here too, two chunks ahead, while the products run: a token a
         // thread, a block of 32 tokens a warp.
         constexpr int HEADS = ONE ? 1 : 2;
@@ -569,80 +696,60 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         };
         if (nch > 0) fetch(0);
         if constexpr (STATES) {
-            tc::tc_before_sync();
-            arrive(S_READY);
+            // The groups' sums, added up in shared memory, a group's once the next one's first half has
+            // its gates (the products are done by then); the last one's on its way out.
+            const int ng = (nch + kGroup - 1) / kGroup;
+            float* dst = p.part + ((int64_t)(sg.slot + sg.j) * p.units + unit) * a.N * 128 + ln;
+            const uint32_t row = sbase + K::OFF_SUM + ln * NP * 4;  // in 16-byte units, swizzled
 #pragma unroll 1
-            for (int c = 0; c < nch; ++c) make_gates(c);
-        } else {
+            for (int hg = 0; hg <= 2 * ng; ++hg) {  // half groups
+                const int end = (hg + 1) * (kGroup / 2) < nch ? (hg + 1) * (kGroup / 2) : nch;
 #pragma unroll 1
-            for (int c = -2; c < nch; ++c) {
-                if (c + 2 < nch) make_gates(c + 2);
-                if (c < 0) continue;
-                const int gs = c % NGR;
-                wait(G_FULL + gs, c / NGR);
-                const float e = gates[2 * gs + (ONE ? 0 : j)].last;
-                if (c > 0) wait(DS_DONE, c - 1);
-                if (c > 0) wait(H_FREE, c - 1);
+                for (int c = hg * (kGroup / 2); c < end; ++c) make_gates(c);
+                const int g = (hg >> 1) - 1;
+                if ((hg & 1) || g < 0) continue;
+                wait(ACC_FULL + (g & 1), g >> 1);
                 __syncwarp();
                 tc::tc_after_sync();
 #pragma unroll 1
                 for (int n0 = 0; n0 < NP; n0 += 16) {
                     float v[16];
-                    uint32_t u[16];
-                    tc::tmem_ld16(lane_base + K::COL_S + n0, v);
+                    tc::tmem_ld16(lane_base + K::col_acc(g) + n0, v);
                     tc::tmem_wait_ld();
-                    const uint32_t at = sbase + K::OFF_H + (n0 / 64) * K::TILE;
+                    if (g > 0)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        tc::st_shared_v4(at + tc::sw128_off(ln, (n0 / 8 + i) & 7), tc::pack_bf16(v[8 * i], v[8 * i + 1]),
-                                         tc::pack_bf16(v[8 * i + 2], v[8 * i + 3]), tc::pack_bf16(v[8 * i + 4], v[8 * i + 5]),
-                                         tc::pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-                    if (nch == 1) {  // what the rounding left, into a tile of x that one chunk leaves free
-                        auto rest = [&](int k) {
-                            const uint32_t w = tc::pack_bf16(v[k], v[k + 1]);
-                            return tc::pack_bf16(v[k] - bf16_lo(w), v[k + 1] - bf16_hi(w));
-                        };
-                        const uint32_t to = sbase + K::OFF_X + (2 + n0 / 64) * K::TILE;
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 o = tc::ld_shared_v4(row + (((n0 / 4 + i) ^ (ln & 7)) << 4));
+                            v[4 * i] += __uint_as_float(o.x);
+                            v[4 * i + 1] += __uint_as_float(o.y);
+                            v[4 * i + 2] += __uint_as_float(o.z);
+                            v[4 * i + 3] += __uint_as_float(o.w);
+                        }
+                    if (g < ng - 1)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            tc::st_shared_v4(to + tc::sw128_off(ln, (n0 / 8 + i) & 7), rest(8 * i), rest(8 * i + 2),
-                                             rest(8 * i + 4), rest(8 * i + 6));
-                    }
+                        for (int i = 0; i < 4; ++i)
+                            tc::st_shared_v4(row + (((n0 / 4 + i) ^ (ln & 7)) << 4), __float_as_uint(v[4 * i]),
+                                             __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                             __float_as_uint(v[4 * i + 3]));
+                    else
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i] * e);
-                    tc::tmem_st16(lane_base + K::COL_S + n0, u);
+                        for (int i = 0; i < 16; ++i)
+                            if (n0 + i < a.N) dst[(n0 + i) * 128] = v[i];
                 }
-                tc::tmem_wait_st();
-                tc::fence_async_smem();
                 tc::tc_before_sync();
-                arrive(S_READY);
+                arrive(ACC_FREE + (g & 1));
             }
-        }
-        // the state that leaves it
-        if (nch > 0) wait(DS_DONE, STATES ? 0 : nch - 1);
-        __syncwarp();
-        tc::tc_after_sync();
-        float* dst = nullptr;
-        if (STATES) {
-            const int64_t at = (int64_t)(sg.slot + sg.j) * p.units + unit;
-            dst = p.part + at * a.N * 128 + ln;
-            step = 128;
-            if (pc == 0) p.part_g[at * 2 + j] = run[ONE ? 0 : j];
-        } else if (a.hT && sg.j == sg.n - 1 && live) {
-            dst = a.hT + hb;
-            step = a.P;
-        }
+            if ((ln & 63) == 0) p.part_g[((int64_t)(sg.slot + sg.j) * p.units + unit) * 2 + (ln >> 6)] = run[ONE ? 0 : ln >> 6];
+        } else {
+            float ep = 0.f;
 #pragma unroll 1
-        for (int n0 = 0; n0 < NP; n0 += 16) {
-            float v[16];
-            tc::tmem_ld16(lane_base + K::COL_S + n0, v);
-            tc::tmem_wait_ld();
-            if (dst)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if (n0 + i < a.N) *dst = v[i];
-                    dst += step;
-                }
+            for (int c = -2; c < nch; ++c) {
+                if (c + 2 < nch) make_gates(c + 2);
+                if (c < 0) continue;
+                wait(G_FULL + c % NGR, c / NGR);
+                ep = advance(c, 0, NS, ep);
+            }
+            leave(0, NS, ep);
         }
     } else if (warp < 24) {
         // =============================================================== Y warps
@@ -817,7 +924,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 const uint32_t lb0 = tc::desc_lo(sbase + K::OFF_B + (c % NB) * K::BT, K::TILE);
                 ready(B_FULL + c % NB, c / NB);
                 if (c == nch - 1 && tail < L) ready(CLEAN, 0);
-                ready(S_READY, STATES ? 0 : c);
+                const int g = STATES ? c / kGroup : 0;
+                const bool first = STATES && c == g * kGroup;  // of a group, whose sum starts anew
+                if (!STATES) ready(S_READY, c);
+                if (first && g > 1) ready(ACC_FREE + (g & 1), (g >> 1) - 1);
+                const uint32_t acc = tmem + (STATES ? K::col_acc(g) : K::COL_S);
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {  // S += (w x)^T B, 32 tokens
                     const int buf = STATES ? k : k & 1;
@@ -825,14 +936,18 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                     go();
                     if (tc::elect_one()) {
                         const uint32_t wx = tmem + (STATES ? K::COL_WX1 : K::COL_WX) + 48 * buf, lb = lb0 + 256 * k;
+                        if (first && k == 0) tc::mma_ts<0>(acc, wx, tc::desc(lb), idS);
+                        else tc::mma_ts<1>(acc, wx, tc::desc(lb), idS);
+                        tc::mma_ts<1>(acc, wx + 8, tc::desc(lb + 128), idS);
 #pragma unroll 1
-                        for (int s = 0; s < 3; ++s)
+                        for (int s = 1; s < 3; ++s)
 #pragma unroll
                             for (int ks = 0; ks < 2; ++ks)
-                                tc::mma_ts<1>(tmem + K::COL_S, wx + 16 * s + 8 * ks, tc::desc(lb + 128 * ks), idS);
+                                tc::mma_ts<1>(acc, wx + 16 * s + 8 * ks, tc::desc(lb + 128 * ks), idS);
                         tc::mma_commit(&bars[XQ_FREE + buf]);
                         if (k == 3) {
-                            if (!STATES || c == nch - 1) tc::mma_commit(&bars[DS_DONE]);
+                            if (!STATES) tc::mma_commit(&bars[DS_DONE]);
+                            else if (c == nch - 1 || c == (g + 1) * kGroup - 1) tc::mma_commit(&bars[ACC_FULL + (g & 1)]);
                             tc::mma_commit(&bars[B_FREE + c % NB]);
                         }
                     }

@@ -415,7 +415,7 @@ gdn_status gdn_accumulate_f32(float* y, const float* x, int64_t n, void* stream)
  * Sequences are independent: what one holds, a NaN included, reaches no other.
  * Within a sequence a NaN or infinity in x reaches y of its head in the whole
  * block of 128 tokens that holds it, the ones before it included, and all later
- * ones; in blocks an infinity in x or Bm may come out as a NaN, in y and in hT.
+ * ones; in blocks an infinity in x, Bm or h0 may come out as a NaN, in y and in hT.
  * Errors: INVALID_ARG (NULL or misaligned pointers, sizes < 0, H % G != 0, a
  * stride shorter than a row, B != 1 with cu_seqlens, a short workspace),
  * UNSUPPORTED (other P or N).  As in gdn_chunk_fwd, offsets outside [0, T] are

@@ -275,3 +275,40 @@ def test_cut_sequences_of_every_form(cuda_device, H, G, P, N, h0, B, T, lens):
     check(d, y, hT)
     y2, hT2 = gdn.ssm_scan(**d)
     assert torch.equal(y, y2) and torch.equal(hT, hT2)
+
+
+@pytest.mark.parametrize("B,T,H,G,P,N,cut,lens", [
+    (37, 8192, 8, 4, 64, 64, False, None), (74, 8192, 2, 2, 128, 128, False, None), (1, 131072, 32, 1, 64, 64, True, None),
+    (2, 40000, 4, 1, 64, 128, True, None), (1, 16384, 296, 148, 64, 64, False, [300, 8000, 0, 5000, 3084])])
+def test_states_that_do_not_decay(cuda_device, B, T, H, G, P, N, cut, lens):
+    # The final state of a head whose decay is nothing, or slow, is a sum over the whole sequence: to fp32's
+    # bound, in sequences that one CTA walks and in cut ones.  hT = sum_t e^(sum of g behind t) dt_t B_t x_t^T.
+    g = torch.Generator("cuda").manual_seed(61)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")
+    row = torch.nn.functional.silu(r(B, T, H * P + 2 * G * N)).bfloat16()
+    n_seq = B if lens is None else len(lens)
+    if cut:
+        assert gdn.ssm_scan_workspace_size(B, B * T, H, G, P, N) > 0
+    A_log = torch.full((H,), -20.0, device="cuda")
+    A_log[1::2] = -4.0
+    d = dict(x=row[..., :H * P].unflatten(-1, (H, P)), Bm=row[..., H * P:H * P + G * N].unflatten(-1, (G, N)),
+             Cm=row[..., H * P + G * N:].unflatten(-1, (G, N)), dt=r(B, T, H).bfloat16(), A_log=A_log,
+             dt_bias=torch.full((H,), -4.0, device="cuda"), h0=0.1 * r(n_seq, H, N, P))
+    if lens is not None:
+        d["cu_seqlens"] = torch.tensor([0] + torch.tensor(lens).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+    hT = gdn.ssm_scan(**d)[1]
+    torch.cuda.synchronize()
+    assert gdn.device_status() == 0
+    ends = [(b * T, (b + 1) * T) for b in range(B)] if lens is None else list(zip(d["cu_seqlens"].tolist(), d["cu_seqlens"].tolist()[1:]))
+    x, Bm, dt = d["x"].flatten(0, 1), d["Bm"].flatten(0, 1), d["dt"].flatten(0, 1)
+    for s in sorted({0, 1 % n_seq, n_seq // 2, n_seq - 1}):
+        for h in (0, 1, H - 1):
+            a, b = ends[s]
+            step = torch.nn.functional.softplus(dt[a:b, h].double() + d["dt_bias"][h].double())
+            decay = -torch.exp(A_log[h].double()) * step
+            behind = decay.flip(0).cumsum(0).flip(0)
+            w = torch.exp(behind - decay) * step
+            ref = Bm[a:b, h // (H // G)].double().T @ (w[:, None] * x[a:b, h].double())
+            ref += d["h0"][s, h].double() * (torch.exp(behind[0]) if b > a else 1.0)
+            err = (hT[s, h].double() - ref).norm()
+            assert err <= (32 + 2 * math.sqrt(b - a)) * E * ref.norm(), (s, h, float(err / ref.norm() / E))
