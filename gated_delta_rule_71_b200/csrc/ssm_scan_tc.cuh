@@ -68,7 +68,7 @@ constexpr int NGR = 3;          // gate ring
 // Where a state keeps the share e of itself over a chunk that adds up to 12 / (1 - e): 50 x 2^-24 at 3/4;
 // where nothing decays to 1.2e-5 of S after 32 chunks, 1.3e-4 after 512.  Above 3/4, therefore, S holds only
 // what the bf16 copy of the state lacks, 2^-9 of it, and the copy is added back in fp32 for the next chunk
-// (3.5e-7 after 32 chunks, 8e-6, the rounding of e, after 512).  Slow heads take 8 % longer by it, others none.
+// (3.5e-7 after 32 chunks, 8e-6, the rounding of e, after 512).  Slow heads take 7 to 11 % longer by it.
 constexpr float kSlow = 0.75f;
 // The first pass has no copy, and no decay between chunks: the sums of kGroup chunks at a time are added up
 // in fp32 in shared memory (37 us for 64 segments of 16 chunks, 35 left in tensor memory; groups of 4: 42).
