@@ -487,7 +487,10 @@ def ssm_scan(x: torch.Tensor, dt: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tens
     x, z [B,T,H,P]; dt [B,T,H]; Bm, Cm [B,T,G,N] (head h reads group h / (H/G)), all of one
     dtype (float32 or bfloat16) and each a slice of evenly spaced rows (the conv row's parts are
     taken as they are); A_log, dt_bias, D [H] fp32; h0 [n_seq,H,N,P] fp32; cu_seqlens int32
-    [n_seq+1] (B == 1).  Returns (y [B,T,H,P] in x's dtype, hT [n_seq,H,N,P] fp32 or None)."""
+    [n_seq+1] (B == 1).  Returns (y [B,T,H,P] in x's dtype, hT [n_seq,H,N,P] fp32 or None).
+    bf16 rows run in blocks of 128 tokens, in which a NaN or infinity in x reaches y of its head at
+    the block's earlier tokens too: in a padded batch x behind a prompt has to be finite (its y and
+    the other operands there do not matter), or the prompts packed."""
     _need(x, "x", contiguous=False)
     dev = x.device
     if x.dtype not in _DT:

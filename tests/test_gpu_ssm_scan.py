@@ -312,3 +312,24 @@ def test_states_that_do_not_decay(cuda_device, B, T, H, G, P, N, cut, lens):
             ref += d["h0"][s, h].double() * (torch.exp(behind[0]) if b > a else 1.0)
             err = (hT[s, h].double() - ref).norm()
             assert err <= (32 + 2 * math.sqrt(b - a)) * E * ref.norm(), (s, h, float(err / ref.norm() / E))
+
+
+@pytest.mark.parametrize("ty", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("P,N", [(64, 128), (128, 64), (64, 64)])
+def test_what_stands_behind_a_prompt_in_a_padded_batch(cuda_device, P, N, bad, ty):
+    # dt, Bm, Cm and z of the tokens behind the prompts hold garbage, and x from the next block of 128 on (bf16):
+    # the prompts' y is what it is without them
+    d = make(3, 430, 4, 2, P, N, ty, 73)
+    ends = (150, 257, 384)
+    for key in ("x", "Bm", "Cm", "dt", "z"):
+        d[key] = d[key].clone()
+        for b, n in enumerate(ends):
+            d[key][b, -(-n // 128) * 128 if key == "x" and ty == torch.bfloat16 else n:] = bad
+    y, _ = gdn.ssm_scan(**d)
+    torch.cuda.synchronize()
+    assert gdn.device_status() == 0
+    for b, n in enumerate(ends):
+        one = {k: v[b:b + 1, :n] if k in ("x", "Bm", "Cm", "dt", "z") else v for k, v in d.items()}
+        one["h0"] = d["h0"][b:b + 1]
+        check(one, y[b:b + 1, :n], None)
