@@ -36,9 +36,9 @@
 // transposing 8 x 8 loads (ldmatrix.trans, st.16x128b).
 //
 // What bounds it: the latency of the chain of hand-overs in a chunk (CB, W, W x; S, C h, y), of
-// which a CTA has one in flight; no unit is full.  A chunk takes 5700 to 7000 cycles
-// an SM (with a gate 7000 or more); the warps' work on CB, x, S and y is some 4700 warp
-// instructions a scheduler (56 % of the issue slots), the products are 3300 cycles at N = 128
+// which a CTA has one in flight; no unit is full.  A chunk takes 5900 cycles an SM at N = 64,
+// some 8500 at N = 128 with a gate; there the warps' work on CB, x, S and y is some 4800 warp
+// instructions a scheduler (57 % of the issue slots), the products are 3400 cycles
 // (36 % of the tensor pipe), HBM runs at a third of its rate.  Where P is 64 or 32 and H / G odd,
 // one CTA of a group has half its lanes empty; P = 32 fills half of each half, and N = 32 runs
 // as 64.
